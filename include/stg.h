@@ -392,6 +392,191 @@ int64_t gemm_scaled_workspace(int32_t a_fmt, int32_t b_fmt, int32_t scale_fmt, i
 int gemm_bounded(const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc,
                  int64_t M, int64_t N, int64_t K, int32_t c_dtype, void* stream);
 
+/* ---- paged key-value cache ------------------------------------------------
+ *
+ * A cache holds the keys (or values) of many sequences in pages of `slots`
+ * tokens: (pages, slots, heads, depth), any non-negative strides with the
+ * last one 1 (one plane of a model's cache, one plane per layer and per keys /
+ * values).  Element types: STG_BF16, STG_F16, or STG_U8, which here means
+ * e4m3 codes (f8e4m3fn), one scale per head.  page_table is STG_I32
+ * (rows, width), last stride 1: token j of row b lives in slot j % slots of
+ * page page_table[b][j / slots].  seq_lens is device int32[rows].  refs is
+ * device int32[pages]: how many table entries name a page; a page is free
+ * when refs <= 0.
+ * Bounds, as for every tile here: a length is taken as min(max(length, 0),
+ * width * slots), and a table entry outside [0, pages) names no page -- its
+ * tokens are not there.  Neither forms an address outside the cache.
+ */
+
+/* Attention of one new token per sequence over its cached tokens.
+ *   q        (rows, q_heads, depth), STG_BF16 or STG_F16, last stride 1.
+ *   k_cache, v_cache  as above, one dtype: q's, or STG_U8 (e4m3 codes).
+ *   page_table, seq_lens  as above; rows = q's.  q_heads must be a multiple of
+ *            heads: query head i attends with cache head i / (q_heads / heads).
+ *   k_scale, v_scale  device float[heads] for STG_U8 caches (a code c of head
+ *            h stands for c * scale[h]), NULL = 1; NULL for other caches.
+ *   window   0, or only the last `window` tokens of a row are attended.
+ *   max_len  a host hint, at least the longest sequence's length where it is
+ *            known (0 = width * slots): it decides how far a sequence is split
+ *            over workgroups, never which tokens are attended.
+ * For row b with the tokens j < seq_lens[b] inside the window and in a page:
+ *   s_j = scale * k_scale * (q . k_j),  out = v_scale * sum_j e^(s_j) v_j /
+ *   sum_j e^(s_j),  lse = ln sum_j e^(s_j)
+ * in fp32 (bf16 / f16 products are exact in it).  A row with no such token
+ * gives out = 0 and lse = -inf; so does one whose scores are all -inf.  Values
+ * in slots that are not attended, NaN among them, have no effect.
+ *   out      (rows, q_heads, depth) of q's dtype, last stride 1.
+ *   lse      device float[rows * q_heads] or NULL.
+ *   workspace  NULL where paged_attention_workspace(...) is 0, else a device
+ *            buffer of at least that many bytes, 256-byte aligned, owned by
+ *            the caller and unused until the stream has run the call.
+ * depth 8 .. 256 (else STG_ERR_UNSUPPORTED). */
+int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, const stg_tensor* v_cache,
+                    const stg_tensor* page_table, const int32_t* seq_lens, const float* k_scale,
+                    const float* v_scale, float scale, int64_t window, int64_t max_len, const stg_tensor* out,
+                    float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of paged_attention for these operands (0: none needed);
+ * a negative status code on invalid arguments.  Host only. */
+int64_t paged_attention_workspace(const stg_tensor* q, const stg_tensor* k_cache, const stg_tensor* page_table,
+                                  int64_t window, int64_t max_len);
+
+/* How queries and keys are normalised and rotated (host structure).
+ *   inv_freq     device float[rotary_dim / 2], the rotation's frequencies.
+ *   rotary_dim   even, 0 .. depth: the leading dimensions of a head that turn;
+ *                the others pass through.
+ *   interleaved  0: dimension i turns with i + rotary_dim / 2; else 2i with 2i+1.
+ *   rope_scale   factor on cosine and sine (1 where none is wanted).
+ *   norm         nonzero: root-mean-square norm over each head's depth first.
+ *   q_weight, k_weight  device [depth] of weight_dtype (STG_F32 or the
+ *                tensors' dtype), or NULL (1); NULL without norm. */
+typedef struct {
+  const float* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t norm;
+  int32_t weight_dtype;
+  float rope_scale;
+  float eps;
+} stg_norm_rope;
+
+/* Host helper: rotation frequencies base^(-2i / rotary_dim), scaled for
+ * contexts `factor` times the original_len positions that a model was trained
+ * on, and the factor on cosine and sine that goes with them.
+ *   STG_ROPE_NONE    as they are.
+ *   STG_ROPE_LINEAR  divided by factor.
+ *   STG_ROPE_NTK     base raised to base * factor^(d / (d - 2)), d = rotary_dim
+ *                    (d = 2, one frequency of 1: nothing to raise).
+ *   STG_ROPE_YARN    frequencies with more than beta_fast turns over
+ *                    original_len stay, those with fewer than beta_slow are
+ *                    divided by factor, linear in the index between (whole
+ *                    indices: floor and ceil of the bounds); rope_scale is
+ *                    0.1 ln(factor) + 1.
+ * inv_freq is a host float[rotary_dim / 2]; rope_scale may be NULL.
+ * STG_ERR_INVALID: odd or negative rotary_dim, base <= 1, factor < 1,
+ * original_len < 1, beta_fast <= beta_slow or beta_slow <= 0, or an unknown
+ * scaling. */
+typedef enum { STG_ROPE_NONE = 0, STG_ROPE_LINEAR = 1, STG_ROPE_NTK = 2, STG_ROPE_YARN = 3 } stg_rope_scaling;
+int rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor, double original_len,
+                     double beta_fast, double beta_slow, float* inv_freq, float* rope_scale);
+
+/* Norm of every query and key head and its rotation by the token's position,
+ * in one pass.  q (tokens, q_heads, depth), k (tokens, k_heads, depth): one
+ * dtype of STG_BF16, STG_F16, STG_F32, last stride 1, any other strides (views
+ * into a fused projection's output).  positions: device int32[tokens], any
+ * value.  For each head x:
+ *   y = norm ? x * w / sqrt(mean(x^2) + eps) : x
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s) for the i-th pair of rotated
+ *   dimensions, c, s = rope_scale * cos, sin of (position * inv_freq[i])
+ * in fp32, rounded once; the angle is reduced in fp64, so it is as exact for
+ * far positions as for near ones.  q_out, k_out: shape and dtype of q, k; each
+ * may be its input itself (the same pointer and strides).
+ * depth 1 .. 1024 (else STG_ERR_UNSUPPORTED). */
+int qk_norm_rope(const stg_tensor* q, const stg_tensor* k, const int32_t* positions, const stg_norm_rope* how,
+                 const stg_tensor* q_out, const stg_tensor* k_out, void* stream);
+
+/* qk_norm_rope whose keys, with the tokens' values, go straight into the pages
+ * of a cache: token t is written as token positions[t] of page table row
+ * rows[t] (rows NULL: row t).  v (tokens, k_heads, depth), q's dtype.
+ * k_cache, v_cache: q's dtype (STG_BF16, STG_F16), or STG_U8, whose codes are
+ * value / scale[h] rounded to nearest even and saturated at +-448 (NaN stays
+ * NaN); the fp32 key is rounded once.  A token whose row, position or page is
+ * out of range writes nothing (its query is still normed and rotated).  Two
+ * tokens with one destination are undefined.  v is copied, not changed. */
+int qk_norm_rope_append(const stg_tensor* q, const stg_tensor* k, const stg_tensor* v, const int32_t* positions,
+                        const stg_norm_rope* how, const int32_t* rows, const stg_tensor* k_cache,
+                        const stg_tensor* v_cache, const stg_tensor* page_table, const float* k_scale,
+                        const float* v_scale, const stg_tensor* q_out, void* stream);
+
+/* Backward of qk_norm_rope.  dq_out, dk_out: gradients of its outputs; q, k,
+ * positions and how as in the forward call (k not yet normed).  With u the
+ * output gradient turned back (angle -t, times rope_scale), x' = x /
+ * sqrt(mean(x^2) + eps):
+ *   norm:  dw = sum over tokens and heads of u x',
+ *          dx = (u w - x' mean(u w x')) / sqrt(mean(x^2) + eps)
+ *   none:  dx = u
+ * dq, dk: shape and dtype of q, k.  dq_weight, dk_weight: device [depth] of
+ * weight_dtype, overwritten, or NULL; NULL without norm.  Sums are fp32, in an
+ * order that depends on the shapes alone, so results repeat bit for bit.
+ * workspace: where a weight gradient is asked for, at least
+ * qk_norm_rope_backward_workspace(...) bytes, 256-byte aligned. */
+int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor* dk_out, const stg_tensor* q,
+                          const stg_tensor* k, const int32_t* positions, const stg_norm_rope* how,
+                          const stg_tensor* dq, const stg_tensor* dk, void* dq_weight, void* dk_weight,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+int64_t qk_norm_rope_backward_workspace(const stg_tensor* q, const stg_tensor* k);
+
+/* Pages.  `cache` here is every plane at once, (planes, pages, elements of a
+ * page), any dtype, last stride 1: pages move in all planes together.
+ * Row and page numbers out of range are skipped.
+ *
+ * pages_copy: page src[i] to page dst[i] (device int32[n]).  A page that is a
+ * destination twice, or a source and a destination, is undefined. */
+int pages_copy(const stg_tensor* cache, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* pages_reserve: room for n_new[b] (device int32[rows]) more tokens in every
+ * row: table entries from seq_lens[b] / slots to (seq_lens[b] + n_new[b] - 1) /
+ * slots that name no page get the lowest free pages, in the order of rows,
+ * then entries, each with refs = 1; other entries and seq_lens stay.  Where
+ * pages run out the remaining entries stay as they are; shortfall (device
+ * int32[1] or NULL) receives how many. */
+int pages_reserve(const stg_tensor* page_table, const int32_t* seq_lens, const int32_t* n_new, int32_t* refs,
+                  int64_t n_pages, int64_t slots, int32_t* shortfall, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* pages_fork: row children[i] becomes a copy of row parents[i] (device
+ * int32[n]).  Full pages are shared (refs + 1); a last page that is not full
+ * is copied to a page of the child's own: the lowest free pages, in the order
+ * of i.  Entries past those become -1.  Where no free page is left, the child
+ * is cut to its full pages (entry -1, shorter length), and shortfall receives
+ * the number of such children.  The child rows' former entries are
+ * overwritten (pages_free them first); a row that is a child twice, or a child
+ * and a parent, is undefined, but nothing outside the operands is touched. */
+int pages_fork(const stg_tensor* cache, const stg_tensor* page_table, int32_t* seq_lens, int32_t* refs,
+               int64_t slots, const int32_t* parents, const int32_t* children, int64_t n, int32_t* shortfall,
+               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* pages_free: rows[i] (device int32[n]) end: refs of every page they name go
+ * down by one per entry, their entries become -1 and their lengths 0.  A row
+ * that is listed twice is freed once. */
+int pages_free(const stg_tensor* page_table, int32_t* seq_lens, int32_t* refs, int64_t n_pages,
+               const int32_t* rows, int64_t n, void* stream);
+
+/* pages_compact: with L live pages (refs > 0), the live pages numbered L and
+ * up, in ascending order, move to the free pages below L, in ascending order:
+ * afterwards pages 0 .. L-1 are live.  Table entries and refs follow.  remap
+ * (device int32[pages]) receives each live page's new number, -1 for a page
+ * that was free. */
+int pages_compact(const stg_tensor* cache, const stg_tensor* page_table, int32_t* refs, int32_t* remap,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of pages_reserve, pages_fork (n = children) and pages_compact
+ * over n_pages pages and n rows; 256-byte aligned device memory.  A negative
+ * status code on invalid arguments.  Host only. */
+int64_t pages_workspace(int64_t n_pages, int64_t n);
+
 /* Kernel tracing, for measurement.  While enabled (on != 0) on the calling
  * thread, every kernel the library launches from that thread records a
  * start/stop hipEvent pair that is part of its own dispatch

@@ -89,6 +89,15 @@ def _load():
         "orc_bf16_to_f64": (ctypes.c_double, [ctypes.c_uint16]),
         "orc_gemm_f64": (None, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64]),
         "orc_gemm_sample_f64": (None, [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _P]),
+        "orc_paged_attention": (None, [_P] * 5 + [_I64] * 7 + [ctypes.c_double, _I64] + [_P] * 4),
+        "orc_norm_rope": (None, [_P] * 4 + [_I64] * 3 + [_I32, _I32, ctypes.c_double, _I32, ctypes.c_double, _P, _P]),
+        "orc_norm_rope_backward": (None, [_P] * 5 + [_I64] * 3 + [_I32, _I32, ctypes.c_double, _I32, ctypes.c_double] +
+                                   [_P] * 4),
+        "orc_pages_copy": (None, [_P, _I64, _I64, _I64, _P, _P, _I64]),
+        "orc_pages_reserve": (_I32, [_P, _I64, _I64, _P, _P, _P, _I64, _I64]),
+        "orc_pages_fork": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P, _I64]),
+        "orc_pages_free": (None, [_P, _I64, _I64, _P, _P, _I64, _P, _I64]),
+        "orc_pages_compact": (None, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -383,3 +392,92 @@ def f64_to_bf16_bits(c64: np.ndarray) -> np.ndarray:
     lib = _load()
     out = np.fromiter((lib.orc_round_to_format(float(v), 8, 7) for v in flat), dtype=np.uint16, count=flat.size)
     return out.reshape(np.shape(c64))
+
+
+# ---- paged key-value cache ---------------------------------------------------
+
+def _f64(x) -> np.ndarray:
+    return np.ascontiguousarray(x, dtype=np.float64)
+
+
+def _i32(x) -> np.ndarray:
+    return np.ascontiguousarray(x, dtype=np.int32)
+
+
+def paged_attention(q, k, v, table, lens, scale, window=0):
+    """(out, lse, abs_out, mag) in fp64: q (rows, q_heads, depth), caches (pages,
+    slots, heads, depth), table (rows, width), lens (rows)."""
+    q, k, v, table, lens = _f64(q), _f64(k), _f64(v), _i32(table), _i32(lens)
+    rows, hq, d = q.shape
+    pages, slots, h, _ = k.shape
+    out, abs_out = np.empty_like(q), np.empty_like(q)
+    lse, mag = np.empty((rows, hq)), np.empty((rows, hq))
+    _load().orc_paged_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(lens), rows, hq, h, d, pages, slots,
+                                table.shape[1], scale, window, _ptr(out), _ptr(lse), _ptr(abs_out), _ptr(mag))
+    return out, lse, abs_out, mag
+
+
+def norm_rope(x, w, positions, inv_freq, interleaved=False, gain=1.0, norm=True, eps=1e-6):
+    """(y, bound) in fp64 for x (tokens, heads, depth); w None: 1."""
+    x, pos = _f64(x), _i32(positions)
+    f = np.ascontiguousarray(inv_freq, dtype=np.float32)
+    w = None if w is None else _f64(w)
+    y, bound = np.empty_like(x), np.empty_like(x)
+    _load().orc_norm_rope(_ptr(x), None if w is None else _ptr(w), _ptr(pos), _ptr(f), *x.shape, 2 * f.size,
+                          int(interleaved), gain, int(norm), eps, _ptr(y), _ptr(bound))
+    return y, bound
+
+
+def norm_rope_backward(dy, x, w, positions, inv_freq, interleaved=False, gain=1.0, norm=True, eps=1e-6):
+    """(dx, bound, dw, abs_dw) in fp64."""
+    dy, x, pos = _f64(dy), _f64(x), _i32(positions)
+    f = np.ascontiguousarray(inv_freq, dtype=np.float32)
+    w = None if w is None else _f64(w)
+    dx, bound = np.empty_like(x), np.empty_like(x)
+    dw, abs_dw = np.empty(x.shape[2]), np.empty(x.shape[2])
+    _load().orc_norm_rope_backward(_ptr(dy), _ptr(x), None if w is None else _ptr(w), _ptr(pos), _ptr(f), *x.shape,
+                                   2 * f.size, int(interleaved), gain, int(norm), eps, _ptr(dx), _ptr(bound),
+                                   _ptr(dw), _ptr(abs_dw))
+    return dx, bound, dw, abs_dw
+
+
+def _pool(cache):
+    """Pointer, planes, pages and bytes of a page of a dense (planes, pages, elements) cache."""
+    assert cache.ndim == 3 and cache.flags.c_contiguous
+    return _ptr(cache), cache.shape[0], cache.shape[1], cache.shape[2] * cache.itemsize
+
+
+def _tables(*arrays):
+    for a in arrays:
+        assert a.dtype == np.int32 and a.flags.c_contiguous
+
+
+def pages_copy(cache, src, dst) -> None:
+    src, dst = _i32(src), _i32(dst)
+    _load().orc_pages_copy(*_pool(cache), _ptr(src), _ptr(dst), src.size)
+
+
+def pages_reserve(table, lens, n_new, refs, slots) -> int:
+    _tables(table, lens, refs)
+    n_new = _i32(n_new)
+    return int(_load().orc_pages_reserve(_ptr(table), *table.shape, _ptr(lens), _ptr(n_new), _ptr(refs), refs.size, slots))
+
+
+def pages_fork(cache, table, lens, refs, slots, parents, children) -> int:
+    _tables(table, lens, refs)
+    parents, children = _i32(parents), _i32(children)
+    return int(_load().orc_pages_fork(*_pool(cache), _ptr(table), *table.shape, _ptr(lens), _ptr(refs), slots,
+                                      _ptr(parents), _ptr(children), parents.size))
+
+
+def pages_free(table, lens, refs, rows) -> None:
+    _tables(table, lens, refs)
+    rows = _i32(rows)
+    _load().orc_pages_free(_ptr(table), *table.shape, _ptr(lens), _ptr(refs), refs.size, _ptr(rows), rows.size)
+
+
+def pages_compact(cache, table, refs) -> np.ndarray:
+    _tables(table, refs)
+    remap = np.empty(refs.size, dtype=np.int32)
+    _load().orc_pages_compact(*_pool(cache), _ptr(table), *table.shape, _ptr(refs), _ptr(remap))
+    return remap

@@ -466,3 +466,249 @@ void orc_gemm_sample_f64(const uint16_t* A, int64_t lda, const uint16_t* B, int6
     out[i] = acc;
   }
 }
+
+/* ---- paged key-value cache --------------------------------------------- */
+
+static int64_t orc_row_length(int32_t len, int64_t width, int64_t slots) {
+  if (len < 0) return 0;
+  return len > width * slots ? width * slots : len;
+}
+
+void orc_paged_attention(const double* q, const double* k, const double* v, const int32_t* table,
+                         const int32_t* lens, int64_t rows, int64_t q_heads, int64_t heads, int64_t depth,
+                         int64_t pages, int64_t slots, int64_t width, double scale, int64_t window, double* out,
+                         double* lse, double* abs_out, double* mag) {
+  for (int64_t b = 0; b < rows; ++b) {
+    const int64_t len = orc_row_length(lens[b], width, slots);
+    const int64_t first = window > 0 && len > window ? len - window : 0;
+    for (int64_t h = 0; h < q_heads; ++h) {
+      const int64_t kh = h / (q_heads / heads);
+      const double* qv = q + (b * q_heads + h) * depth;
+      double* o = out + (b * q_heads + h) * depth;
+      double* ao = abs_out + (b * q_heads + h) * depth;
+      double top = -INFINITY, sum = 0.0, big = 0.0;
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass)
+          for (int64_t d = 0; d < depth; ++d) o[d] = ao[d] = 0.0;
+        for (int64_t j = first; j < len; ++j) {
+          const int32_t page = table[b * width + j / slots];
+          if (page < 0 || page >= pages) continue;
+          const int64_t at = ((page * slots + j % slots) * heads + kh) * depth;
+          double s = 0.0, a = 0.0;
+          for (int64_t d = 0; d < depth; ++d) {
+            s += qv[d] * k[at + d];
+            a += fabs(qv[d] * k[at + d]);
+          }
+          s *= scale;
+          if (!pass) {
+            if (s > top) top = s;
+            if (a * fabs(scale) > big) big = a * fabs(scale);
+          } else {
+            const double p = exp(s - top);
+            sum += p;
+            for (int64_t d = 0; d < depth; ++d) {
+              o[d] += p * v[at + d];
+              ao[d] += p * fabs(v[at + d]);
+            }
+          }
+        }
+        if (top == -INFINITY) break;
+      }
+      mag[b * q_heads + h] = big;
+      lse[b * q_heads + h] = top == -INFINITY ? -INFINITY : top + log(sum);
+      for (int64_t d = 0; d < depth; ++d) {
+        o[d] = top == -INFINITY ? 0.0 : o[d] / sum;
+        ao[d] = top == -INFINITY ? 0.0 : ao[d] / sum;
+      }
+    }
+  }
+}
+
+/* dimensions (a, b) of pair i */
+static void orc_pair(int64_t i, int32_t rotary, int32_t interleaved, int64_t* a, int64_t* b) {
+  *a = interleaved ? 2 * i : i;
+  *b = interleaved ? 2 * i + 1 : i + rotary / 2;
+}
+
+void orc_norm_rope(const double* x, const double* w, const int32_t* positions, const float* inv_freq, int64_t tokens,
+                   int64_t heads, int64_t depth, int32_t rotary, int32_t interleaved, double gain, int32_t norm,
+                   double eps, double* y, double* bound) {
+  for (int64_t t = 0; t < tokens; ++t)
+    for (int64_t h = 0; h < heads; ++h) {
+      const double* xv = x + (t * heads + h) * depth;
+      double* yv = y + (t * heads + h) * depth;
+      double* bv = bound + (t * heads + h) * depth;
+      double r = 1.0;
+      if (norm) {
+        double ss = 0.0;
+        for (int64_t d = 0; d < depth; ++d) ss += xv[d] * xv[d];
+        r = 1.0 / sqrt(ss / (double)depth + eps);
+      }
+      for (int64_t d = 0; d < depth; ++d) {
+        yv[d] = norm ? xv[d] * r * (w ? w[d] : 1.0) : xv[d];
+        bv[d] = fabs(yv[d]);
+      }
+      for (int64_t i = 0; i < rotary / 2; ++i) {
+        int64_t a, b;
+        orc_pair(i, rotary, interleaved, &a, &b);
+        const long double angle = (long double)positions[t] * (long double)inv_freq[i];
+        const double c = gain * (double)cosl(angle), s = gain * (double)sinl(angle);
+        const double ya = yv[a], yb = yv[b];
+        yv[a] = ya * c - yb * s;
+        yv[b] = yb * c + ya * s;
+        bv[a] = bv[b] = fabs(gain) * (fabs(ya) + fabs(yb));
+      }
+    }
+}
+
+void orc_norm_rope_backward(const double* dy, const double* x, const double* w, const int32_t* positions,
+                            const float* inv_freq, int64_t tokens, int64_t heads, int64_t depth, int32_t rotary,
+                            int32_t interleaved, double gain, int32_t norm, double eps, double* dx, double* bound,
+                            double* dw, double* abs_dw) {
+  if (dw)
+    for (int64_t d = 0; d < depth; ++d) dw[d] = abs_dw[d] = 0.0;
+  for (int64_t t = 0; t < tokens; ++t)
+    for (int64_t h = 0; h < heads; ++h) {
+      const double* g = dy + (t * heads + h) * depth;
+      const double* xv = x + (t * heads + h) * depth;
+      double* u = dx + (t * heads + h) * depth;
+      double* m = bound + (t * heads + h) * depth;
+      for (int64_t d = 0; d < depth; ++d) {
+        u[d] = g[d];
+        m[d] = fabs(g[d]);
+      }
+      for (int64_t i = 0; i < rotary / 2; ++i) {
+        int64_t a, b;
+        orc_pair(i, rotary, interleaved, &a, &b);
+        const long double angle = (long double)positions[t] * (long double)inv_freq[i];
+        const double c = gain * (double)cosl(angle), s = gain * (double)sinl(angle);
+        u[a] = g[a] * c + g[b] * s; /* the transposed rotation */
+        u[b] = g[b] * c - g[a] * s;
+        m[a] = m[b] = fabs(gain) * (fabs(g[a]) + fabs(g[b]));
+      }
+      if (!norm) continue;
+      double ss = 0.0, inner = 0.0, abs_inner = 0.0;
+      for (int64_t d = 0; d < depth; ++d) ss += xv[d] * xv[d];
+      const double r = 1.0 / sqrt(ss / (double)depth + eps);
+      for (int64_t d = 0; d < depth; ++d) {
+        const double xn = xv[d] * r, wd = w ? w[d] : 1.0;
+        if (dw) {
+          dw[d] += u[d] * xn;
+          abs_dw[d] += m[d] * fabs(xn);
+        }
+        inner += u[d] * wd * xn;
+        abs_inner += m[d] * fabs(wd * xn);
+      }
+      for (int64_t d = 0; d < depth; ++d) {
+        const double xn = xv[d] * r, wd = w ? w[d] : 1.0;
+        u[d] = r * (u[d] * wd - xn * inner / (double)depth);
+        m[d] = r * (m[d] * fabs(wd) + fabs(xn) * abs_inner / (double)depth);
+      }
+    }
+}
+
+static int orc_in(int32_t i, int64_t n) { return i >= 0 && i < n; }
+
+void orc_pages_copy(uint8_t* cache, int64_t planes, int64_t pages, int64_t page_bytes, const int32_t* src,
+                    const int32_t* dst, int64_t n) {
+  for (int64_t i = 0; i < n; ++i) {
+    if (!orc_in(src[i], pages) || !orc_in(dst[i], pages)) continue;
+    for (int64_t p = 0; p < planes; ++p)
+      memcpy(cache + (p * pages + dst[i]) * page_bytes, cache + (p * pages + src[i]) * page_bytes, (size_t)page_bytes);
+  }
+}
+
+/* The lowest free page at or after *from, or -1; *from moves past it. */
+static int32_t orc_take(const int32_t* refs, int64_t pages, int64_t* from) {
+  while (*from < pages) {
+    const int64_t p = (*from)++;
+    if (refs[p] <= 0) return (int32_t)p;
+  }
+  return -1;
+}
+
+int32_t orc_pages_reserve(int32_t* table, int64_t rows, int64_t width, const int32_t* lens, const int32_t* n_new,
+                          int32_t* refs, int64_t pages, int64_t slots) {
+  int32_t missing = 0;
+  int64_t from = 0;
+  for (int64_t b = 0; b < rows; ++b) {
+    const int64_t len = orc_row_length(lens[b], width, slots);
+    for (int64_t j = len; j < len + (n_new[b] > 0 ? n_new[b] : 0) && j < width * slots; ++j) {
+      int32_t* e = table + b * width + j / slots;
+      if ((j > len && j % slots) || orc_in(*e, pages)) continue;
+      const int32_t page = orc_take(refs, pages, &from); /* pages taken here lie before `from` */
+      if (page < 0) {
+        ++missing;
+      } else {
+        *e = page;
+        refs[page] = 1;
+      }
+    }
+  }
+  return missing;
+}
+
+int32_t orc_pages_fork(uint8_t* cache, int64_t planes, int64_t pages, int64_t page_bytes, int32_t* table,
+                       int64_t rows, int64_t width, int32_t* lens, int32_t* refs, int64_t slots,
+                       const int32_t* parents, const int32_t* children, int64_t n) {
+  int32_t missing = 0;
+  int64_t from = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const int32_t p = parents[i], c = children[i];
+    if (!orc_in(p, rows) || !orc_in(c, rows) || p == c) continue;
+    int64_t len = orc_row_length(lens[p], width, slots);
+    for (int64_t j = 0; j < width; ++j) {
+      const int32_t e = table[p * width + j];
+      int32_t to = -1;
+      if (j < len / slots && orc_in(e, pages)) {
+        to = e;
+        refs[e] += 1;
+      } else if (j == len / slots && len % slots && orc_in(e, pages)) {
+        to = orc_take(refs, pages, &from);
+        if (to >= 0) {
+          refs[to] = 1;
+          orc_pages_copy(cache, planes, pages, page_bytes, &e, &to, 1);
+        } else {
+          ++missing;
+          len -= len % slots;
+        }
+      }
+      table[c * width + j] = to;
+    }
+    lens[c] = (int32_t)len;
+  }
+  return missing;
+}
+
+void orc_pages_free(int32_t* table, int64_t rows, int64_t width, int32_t* lens, int32_t* refs, int64_t pages,
+                    const int32_t* which, int64_t n) {
+  for (int64_t i = 0; i < n; ++i) {
+    if (!orc_in(which[i], rows)) continue;
+    for (int64_t j = 0; j < width; ++j) {
+      int32_t* e = table + which[i] * width + j;
+      if (orc_in(*e, pages)) refs[*e] -= 1;
+      *e = -1;
+    }
+    lens[which[i]] = 0;
+  }
+}
+
+void orc_pages_compact(uint8_t* cache, int64_t planes, int64_t pages, int64_t page_bytes, int32_t* table,
+                       int64_t rows, int64_t width, int32_t* refs, int32_t* remap) {
+  int64_t live = 0, to = 0;
+  for (int64_t p = 0; p < pages; ++p) {
+    live += refs[p] > 0;
+    remap[p] = refs[p] > 0 ? (int32_t)p : -1;
+  }
+  for (int64_t p = live; p < pages; ++p) {
+    if (refs[p] <= 0) continue;
+    while (refs[to] > 0) ++to;
+    const int32_t a = (int32_t)p, b = (int32_t)to;
+    orc_pages_copy(cache, planes, pages, page_bytes, &a, &b, 1);
+    refs[b] = refs[a];
+    refs[a] = 0;
+    remap[a] = b;
+  }
+  for (int64_t i = 0; i < rows * width; ++i)
+    if (orc_in(table[i], pages) && remap[table[i]] >= 0) table[i] = remap[table[i]];
+}

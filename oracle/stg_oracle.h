@@ -226,6 +226,52 @@ void orc_gemm_sample_f64(const uint16_t* A, int64_t lda, const uint16_t* B, int6
                          int64_t K, const int64_t* rows, const int64_t* cols, int64_t n,
                          double* out);
 
+/* ---- paged key-value cache ----
+ * All values in fp64 (the caller decodes them); caches are dense (pages, slots,
+ * heads, depth).  Token j of row b is in slot j % slots of page
+ * table[b*width + j/slots]; a length is clamped to [0, width*slots]; a table
+ * entry outside [0, pages) names no page and its tokens are not there. */
+
+/* Attention of one token per row: with s_j = scale * (q . k_j) over the row's
+ * tokens inside the window (0: all), out = sum e^(s_j) v_j / sum e^(s_j), lse =
+ * ln sum e^(s_j); no token: out 0, lse -inf.  Query head i uses cache head
+ * i / (q_heads / heads).  For error bounds: abs_out is the same average of
+ * |v_j|, mag the largest scale * sum |q_d k_jd|. */
+void orc_paged_attention(const double* q, const double* k, const double* v, const int32_t* table,
+                         const int32_t* lens, int64_t rows, int64_t q_heads, int64_t heads, int64_t depth,
+                         int64_t pages, int64_t slots, int64_t width, double scale, int64_t window, double* out,
+                         double* lse, double* abs_out, double* mag);
+
+/* Norm and rotation of x (tokens, heads, depth): y = norm ? x w / sqrt(mean
+ * x^2 + eps) : x; pair i of the leading rotary dimensions -- (i, i + rotary/2),
+ * interleaved (2i, 2i+1) -- turns by position * inv_freq[i], times gain.
+ * w may be NULL (1).  bound (same shape): the sum of the magnitudes that enter
+ * each result. */
+void orc_norm_rope(const double* x, const double* w, const int32_t* positions, const float* inv_freq, int64_t tokens,
+                   int64_t heads, int64_t depth, int32_t rotary, int32_t interleaved, double gain, int32_t norm,
+                   double eps, double* y, double* bound);
+
+/* Its gradients: dx, and dw (may be NULL) with abs_dw, the sum of its terms'
+ * magnitudes.  bound: magnitudes that enter each dx. */
+void orc_norm_rope_backward(const double* dy, const double* x, const double* w, const int32_t* positions,
+                            const float* inv_freq, int64_t tokens, int64_t heads, int64_t depth, int32_t rotary,
+                            int32_t interleaved, double gain, int32_t norm, double eps, double* dx, double* bound,
+                            double* dw, double* abs_dw);
+
+/* Page operations, in place, one step after another.  cache is dense (planes,
+ * pages, page_bytes). */
+void orc_pages_copy(uint8_t* cache, int64_t planes, int64_t pages, int64_t page_bytes, const int32_t* src,
+                    const int32_t* dst, int64_t n);
+int32_t orc_pages_reserve(int32_t* table, int64_t rows, int64_t width, const int32_t* lens, const int32_t* n_new,
+                          int32_t* refs, int64_t pages, int64_t slots);
+int32_t orc_pages_fork(uint8_t* cache, int64_t planes, int64_t pages, int64_t page_bytes, int32_t* table,
+                       int64_t rows, int64_t width, int32_t* lens, int32_t* refs, int64_t slots,
+                       const int32_t* parents, const int32_t* children, int64_t n);
+void orc_pages_free(int32_t* table, int64_t rows, int64_t width, int32_t* lens, int32_t* refs, int64_t pages,
+                    const int32_t* which, int64_t n);
+void orc_pages_compact(uint8_t* cache, int64_t planes, int64_t pages, int64_t page_bytes, int32_t* table,
+                       int64_t rows, int64_t width, int32_t* refs, int32_t* remap);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,10 +15,23 @@ from ._binding import (  # noqa: F401
     gemm_scaled,
     gemm_scaled_workspace,
     load_library,
+    paged_attention,
+    paged_attention_workspace,
+    pages_compact,
+    pages_copy,
+    pages_fork,
+    pages_free,
+    pages_reserve,
+    pages_workspace,
     prepare,
+    qk_norm_rope,
+    qk_norm_rope_append,
+    qk_norm_rope_backward,
+    qk_norm_rope_backward_workspace,
     ragged_tile_load,
     ragged_tile_store,
     ragged_tile_schedule,
+    rope_frequencies,
     stg_tile_grid,
     stg_trace_enable,
     stg_trace_read,

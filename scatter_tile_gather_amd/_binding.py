@@ -69,6 +69,20 @@ _SIGNATURES = {
     "gemm_scaled_ws": (ctypes.c_int, [_P, _I32, _I64, _P, _I64, _P, _I32, _I64, _P, _I64, _I32, _I64, _P, _I64, _P,
                                       _I64, _I64, _I64, _I64, _P, _I64, _P]),
     "gemm_scaled_workspace": (_I64, [_I32, _I32, _I32, _I64, _I64, _I64, _I64]),
+    "paged_attention": (ctypes.c_int, [_TP, _TP, _TP, _TP, _P, _P, _P, ctypes.c_float, _I64, _I64, _TP, _P, _P, _I64, _P]),
+    "paged_attention_workspace": (_I64, [_TP, _TP, _TP, _I64, _I64]),
+    "rope_frequencies": (ctypes.c_int, [_I32, ctypes.c_double, _I32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                        ctypes.c_double, _P, _P]),
+    "qk_norm_rope": (ctypes.c_int, [_TP, _TP, _P, _P, _TP, _TP, _P]),
+    "qk_norm_rope_append": (ctypes.c_int, [_TP, _TP, _TP, _P, _P, _P, _TP, _TP, _TP, _P, _P, _TP, _P]),
+    "qk_norm_rope_backward": (ctypes.c_int, [_TP, _TP, _TP, _TP, _P, _P, _TP, _TP, _P, _P, _P, _I64, _P]),
+    "qk_norm_rope_backward_workspace": (_I64, [_TP, _TP]),
+    "pages_copy": (ctypes.c_int, [_TP, _P, _P, _I64, _P]),
+    "pages_reserve": (ctypes.c_int, [_TP, _P, _P, _P, _I64, _I64, _P, _P, _I64, _P]),
+    "pages_fork": (ctypes.c_int, [_TP, _TP, _P, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P]),
+    "pages_free": (ctypes.c_int, [_TP, _P, _P, _I64, _P, _I64, _P]),
+    "pages_compact": (ctypes.c_int, [_TP, _TP, _P, _P, _P, _I64, _P]),
+    "pages_workspace": (_I64, [_I64, _I64]),
     "stg_trace_enable": (ctypes.c_int, [ctypes.c_int]),
     "stg_trace_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float)]),
 }
@@ -661,3 +675,283 @@ def gemm_scaled(A, a_fmt: str, a_scale, Bt, b_fmt: str, b_scale, K: int, block: 
                               SCALE_FORMATS[scale_fmt], block, accp, ldacc, out.data_ptr(), out.stride(0), M, N, K,
                               ws_ptr, ws_n, _stream(stream, A))
     return out
+
+
+# ---- paged key-value cache ---------------------------------------------------
+
+def _int_array(x, n, name: str):
+    """Pointer of a contiguous int32 device tensor of n entries."""
+    torch = _torch()
+    if x.numel() != n:
+        raise ValueError(f"{name} must hold {n} entries")
+    return _dev_array(x, torch.int32, name)
+
+
+def _cache_desc(t, name: str) -> bytes:
+    """A cache's stg_tensor; e4m3 tensors travel as their bytes."""
+    torch = _torch()
+    return _desc(t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t, name)
+
+
+def _scales(x, heads: int, name: str):
+    torch = _torch()
+    if x is None:
+        return None
+    if x.numel() != heads:
+        raise ValueError(f"{name} must hold one entry per cache head")
+    return _dev_array(x, torch.float32, name)
+
+
+def _bytes_or_raise(n: int) -> int:
+    if n < 0:
+        raise StgError(-n, load_library().stg_last_error().decode())
+    return n
+
+
+def _ws(workspace, nbytes, like, stream):
+    """(pointer, bytes) of a workspace argument: None, a device tensor, or
+    "auto", which asks nbytes() and allocates that much."""
+    if isinstance(workspace, str) and workspace == "auto":
+        nb = nbytes()
+        workspace = _workspace(nb, like.device, stream) if nb else None
+    if workspace is None:
+        return None, 0
+    _on_gpu(workspace, "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def paged_attention_workspace(q, k_cache, page_table, window: int = 0, max_len: int = 0) -> int:
+    """Bytes of workspace paged_attention needs for these operands (0: none)."""
+    return _bytes_or_raise(int(load_library().paged_attention_workspace(
+        _desc(q, "q"), _cache_desc(k_cache, "k_cache"), _desc(page_table, "page_table"), window, max_len)))
+
+
+def paged_attention(q, k_cache, v_cache, page_table, seq_lens, scale=None, window: int = 0, k_scale=None, v_scale=None,
+                    max_len: int = 0, out=None, lse=None, workspace="auto", stream=None):
+    """Attention of one new token per row over its cached tokens.  q: (rows,
+    q_heads, depth) bf16 or f16; caches: (pages, slots, heads, depth) of q's
+    dtype, or float8_e4m3fn / uint8 (e4m3 codes, with k_scale and v_scale per
+    head); page_table: int32 (rows, width); seq_lens: int32 (rows).  scale
+    defaults to depth ** -0.5; window > 0 attends to the last `window` tokens;
+    max_len: a hint, at least the longest length (0: the table's room).  lse:
+    a float32 (rows, q_heads) tensor that receives the log of each row's sum."""
+    torch = _torch()
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be (rows, heads, depth) and the caches (pages, slots, heads, depth)")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+    lp = None
+    if lse is not None:
+        if tuple(lse.shape) != tuple(q.shape[:2]):
+            raise ValueError("lse must be (rows, q_heads)")
+        lp = _dev_array(lse, torch.float32, "lse")
+    heads = k_cache.shape[2]
+    qd, kd, vd, td = _desc(q, "q"), _cache_desc(k_cache, "k_cache"), _cache_desc(v_cache, "v_cache"), _desc(page_table, "page_table")
+    ws, wn = _ws(workspace, lambda: paged_attention_workspace(q, k_cache, page_table, window, max_len), q, stream)
+    _call("paged_attention", qd, kd, vd, td, _int_array(seq_lens, q.shape[0], "seq_lens"),
+          _scales(k_scale, heads, "k_scale"), _scales(v_scale, heads, "v_scale"), float(scale), window, max_len,
+          _desc(out, "out"), lp, ws, wn, _stream(stream, q))
+    return out
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Host helper: (float32 numpy array of rotary_dim / 2 frequencies, the
+    factor on cosine and sine) for a rotation scaled to longer contexts."""
+    freq = np.zeros(max(rotary_dim, 0) // 2, dtype=np.float32)
+    gain = ctypes.c_float(1.0)
+    _check(load_library().rope_frequencies(rotary_dim, base, ROPE_SCALINGS[scaling], factor, original_len, beta_fast,
+                                           beta_slow, freq.ctypes.data if freq.size else None, ctypes.byref(gain)))
+    return freq, gain.value
+
+
+# stg_norm_rope's bytes
+_HOW = struct.Struct("<QQQiiiiff")
+
+
+def _how(q, inv_freq, q_weight, k_weight, eps, norm, interleaved, rope_scale):
+    torch = _torch()
+    depth, wd = q.shape[2], None
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        _on_gpu(w, name)
+        if w.dim() != 1 or w.shape[0] != depth or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous ({depth},) tensor")
+        if wd is not None and w.dtype != wd:
+            raise ValueError("q_weight and k_weight must have one dtype")
+        wd = w.dtype
+    code = STG_F32 if wd is None else _dtype_code(q_weight if q_weight is not None else k_weight)
+    n = inv_freq.numel()
+    fp = _dev_array(inv_freq, torch.float32, "inv_freq") if n else 0
+    ptr = lambda w: 0 if w is None else w.data_ptr()  # noqa: E731
+    return _HOW.pack(fp, ptr(q_weight), ptr(k_weight), 2 * n, 1 if interleaved else 0, 1 if norm else 0, code,
+                     float(rope_scale), float(eps))
+
+
+def _check_qk(q, k):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be (tokens, heads, depth)")
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                 interleaved: bool = False, rope_scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Norm of each query and key head and its rotation by the token's position.
+    q, k: (tokens, heads, depth) bf16, f16 or f32, unit depth stride;
+    positions: int32 (tokens); inv_freq: float32 (rotary_dim / 2), see
+    rope_frequencies.  Returns (q_out, k_out); either may be its input."""
+    torch = _torch()
+    _check_qk(q, k)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    how = _how(q, inv_freq, q_weight, k_weight, eps, norm, interleaved, rope_scale)
+    _call("qk_norm_rope", _desc(q, "q"), _desc(k, "k"), _int_array(positions, q.shape[0], "positions"), how,
+          _desc(q_out, "q_out"), _desc(k_out, "k_out"), _stream(stream, q))
+    return q_out, k_out
+
+
+def qk_norm_rope_append(q, k, v, positions, inv_freq, k_cache, v_cache, page_table, rows=None, k_scale=None,
+                        v_scale=None, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                        interleaved: bool = False, rope_scale: float = 1.0, q_out=None, stream=None):
+    """qk_norm_rope that writes the keys, and the values v as they are, into the
+    pages of a cache: token t becomes token positions[t] of page-table row
+    rows[t] (rows None: row t).  Caches as for paged_attention; tokens whose
+    row, position or page is out of range write nothing.  Returns q_out."""
+    torch = _torch()
+    _check_qk(q, k)
+    if k_cache.dim() != 4:
+        raise ValueError("caches must be (pages, slots, heads, depth)")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    heads, n = k_cache.shape[2], q.shape[0]
+    how = _how(q, inv_freq, q_weight, k_weight, eps, norm, interleaved, rope_scale)
+    _call("qk_norm_rope_append", _desc(q, "q"), _desc(k, "k"), _desc(v, "v"), _int_array(positions, n, "positions"), how,
+          None if rows is None else _int_array(rows, n, "rows"), _cache_desc(k_cache, "k_cache"),
+          _cache_desc(v_cache, "v_cache"), _desc(page_table, "page_table"), _scales(k_scale, heads, "k_scale"),
+          _scales(v_scale, heads, "v_scale"), _desc(q_out, "q_out"), _stream(stream, q))
+    return q_out
+
+
+def qk_norm_rope_backward_workspace(q, k) -> int:
+    """Bytes of workspace the backward's weight gradients need."""
+    return _bytes_or_raise(int(load_library().qk_norm_rope_backward_workspace(_desc(q, "q"), _desc(k, "k"))))
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                          norm: bool = True, interleaved: bool = False, rope_scale: float = 1.0, dq=None, dk=None,
+                          dq_weight=None, dk_weight=None, workspace="auto", stream=None):
+    """Gradients of qk_norm_rope at q, k (its inputs) for the output gradients
+    dq_out, dk_out: returns (dq, dk, dq_weight, dk_weight).  A weight gradient
+    is of its weight's dtype, None where there is no weight."""
+    torch = _torch()
+    _check_qk(q, k)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    how = _how(q, inv_freq, q_weight, k_weight, eps, norm, interleaved, rope_scale)
+    grads = []
+    for w, g, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None and g is not None:
+            raise ValueError(f"{name} without its weight")
+        if w is not None and g is None:
+            g = torch.empty_like(w)
+        if w is not None and g.numel() != w.numel():
+            raise ValueError(f"{name} must have its weight's shape")
+        grads.append((g, None if w is None else _dev_array(g, w.dtype, name)))
+    (dqw, dqp), (dkw, dkp) = grads
+    ws, wn = (None, 0) if dqp is None and dkp is None else _ws(
+        workspace, lambda: qk_norm_rope_backward_workspace(q, k), q, stream)
+    _call("qk_norm_rope_backward", _desc(dq_out, "dq_out"), _desc(dk_out, "dk_out"), _desc(q, "q"), _desc(k, "k"),
+          _int_array(positions, q.shape[0], "positions"), how, _desc(dq, "dq"), _desc(dk, "dk"), dqp, dkp, ws, wn,
+          _stream(stream, q))
+    return dq, dk, dqw, dkw
+
+
+def _planes(cache):
+    if cache.dim() != 3:
+        raise ValueError("cache must be (planes, pages, elements of a page)")
+    return _cache_desc(cache, "cache")
+
+
+def _table(page_table):
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (rows, width)")
+    return _desc(page_table, "page_table")
+
+
+def _one_int(x, name: str):
+    return None if x is None else _int_array(x, 1, name)
+
+
+def pages_workspace(n_pages: int, n: int) -> int:
+    """Bytes of workspace for pages_reserve (n = rows), pages_fork (n =
+    children) and pages_compact (n = 0) over n_pages pages."""
+    return _bytes_or_raise(int(load_library().pages_workspace(n_pages, n)))
+
+
+def pages_copy(cache, src, dst, stream=None):
+    """Page src[i] -> page dst[i] (int32) in every plane of cache (planes,
+    pages, elements of a page); pairs out of range are skipped."""
+    n = src.numel()
+    _call("pages_copy", _planes(cache), _int_array(src, n, "src"), _int_array(dst, n, "dst"), n, _stream(stream, cache))
+    return cache
+
+
+def pages_reserve(page_table, seq_lens, n_new, refs, slots: int, shortfall=None, workspace="auto", stream=None):
+    """Pages for n_new[b] (int32) more tokens in every row: the lowest free
+    pages, in the order of rows.  Updates page_table and refs; shortfall (int32,
+    one entry) receives how many entries got none.  Returns page_table."""
+    td = _table(page_table)
+    rows, n = page_table.shape[0], refs.numel()
+    ws, wn = _ws(workspace, lambda: pages_workspace(n, rows), page_table, stream)
+    _call("pages_reserve", td, _int_array(seq_lens, rows, "seq_lens"), _int_array(n_new, rows, "n_new"),
+          _int_array(refs, n, "refs"), n, slots, _one_int(shortfall, "shortfall"), ws, wn, _stream(stream, page_table))
+    return page_table
+
+
+def pages_fork(cache, page_table, seq_lens, refs, slots: int, parents, children, shortfall=None, workspace="auto",
+               stream=None):
+    """Row children[i] becomes a copy of row parents[i] (int32): full pages are
+    shared, a partly filled last page is copied to the lowest free page.
+    Updates cache, page_table, seq_lens and refs; shortfall (int32, one entry)
+    receives how many children were cut to their full pages for want of a
+    page.  Returns page_table."""
+    cd, td, n = _planes(cache), _table(page_table), parents.numel()
+    pages = cache.shape[1]
+    ws, wn = _ws(workspace, lambda: pages_workspace(pages, n), cache, stream)
+    _call("pages_fork", cd, td, _int_array(seq_lens, page_table.shape[0], "seq_lens"),
+          _int_array(refs, pages, "refs"), slots, _int_array(parents, n, "parents"),
+          _int_array(children, n, "children"), n, _one_int(shortfall, "shortfall"), ws, wn, _stream(stream, cache))
+    return page_table
+
+
+def pages_free(page_table, seq_lens, refs, rows, stream=None):
+    """The sequences in rows (int32) end: their pages' refs go down, their
+    entries become -1, their lengths 0.  Returns page_table."""
+    n = rows.numel()
+    _call("pages_free", _table(page_table), _int_array(seq_lens, page_table.shape[0], "seq_lens"),
+          _int_array(refs, refs.numel(), "refs"), refs.numel(), _int_array(rows, n, "rows"), n,
+          _stream(stream, page_table))
+    return page_table
+
+
+def pages_compact(cache, page_table, refs, remap=None, workspace="auto", stream=None):
+    """Moves the live pages to the front of the pool and rewrites page_table
+    and refs.  Returns remap (int32, one entry per page): a live page's new
+    number, -1 for a page that was free."""
+    torch = _torch()
+    cd, td, pages = _planes(cache), _table(page_table), cache.shape[1]
+    if remap is None:
+        remap = torch.empty(pages, dtype=torch.int32, device=cache.device)
+    ws, wn = _ws(workspace, lambda: pages_workspace(pages, 0), cache, stream)
+    _call("pages_compact", cd, td, _int_array(refs, pages, "refs"), _int_array(remap, pages, "remap"), ws, wn,
+          _stream(stream, cache))
+    return remap

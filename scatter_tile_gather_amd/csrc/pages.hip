@@ -1,0 +1,651 @@
+// Pages of a key-value cache: copying, reserving, forking, freeing and
+// compacting them, with the page table, lengths and reference counts on the
+// device throughout (no host synchronisation, so a decode loop that calls them
+// can be captured into a graph).
+//
+// A page is free when its reference count is 0.  There is no list of free
+// pages to keep: the k-th free page, counted from the lowest number, is found
+// by a scan over the counts, so which page an operation takes depends on the
+// state alone and never on the order in which threads ran.
+//
+// What bounds them: moving a page reads and writes planes * page bytes once
+// (HBM); the tables are a few kilobytes, and their kernels are latency.  So
+// each operation is two launches: a plan (the scan) and an apply, in which the
+// workgroups that copy pages also write the tables.
+#include "stg_internal.h"
+
+namespace stg {
+
+constexpr int64_t kMaxCount = (int64_t(1) << 31) - 1;
+
+int check_page_table(const char* what, const stg_tensor* t) {
+  if (int rc = check_tensor(t, "page_table")) return rc;
+  if (t->dtype != STG_I32) return fail(STG_ERR_UNSUPPORTED, "%s: page_table must be int32", what);
+  if (t->rank != 2 || (t->shape[1] > 1 && t->stride[1] != 1))
+    return fail(STG_ERR_INVALID, "%s: page_table must be (rows, width) with unit column stride", what);
+  if (t->shape[0] > kMaxCount || t->shape[1] > kMaxCount)
+    return fail(STG_ERR_RANGE, "%s: page_table exceeds 2^31 - 1 rows or entries", what);
+  if (t->shape[0] > 1 && t->stride[0] < t->shape[1])
+    return fail(STG_ERR_INVALID, "%s: page_table rows overlap", what);
+  return STG_OK;
+}
+
+int check_paged_cache(const char* what, const stg_tensor* k_cache, const stg_tensor* v_cache,
+                      const stg_tensor* page_table) {
+  if (int rc = check_tensor(k_cache, "k_cache")) return rc;
+  if (int rc = check_tensor(v_cache, "v_cache")) return rc;
+  if (int rc = check_page_table(what, page_table)) return rc;
+  for (const stg_tensor* c : {k_cache, v_cache}) {
+    if (c->dtype != STG_BF16 && c->dtype != STG_F16 && c->dtype != STG_U8)
+      return fail(STG_ERR_UNSUPPORTED, "%s: caches must be bf16, f16 or u8 (e4m3 codes)", what);
+    if (c->rank != 4 || (c->shape[3] > 1 && c->stride[3] != 1))
+      return fail(STG_ERR_INVALID, "%s: caches must be (pages, slots, heads, depth) with unit depth stride", what);
+    if (c->shape[0] > kMaxCount || c->shape[1] > kMaxCount)
+      return fail(STG_ERR_RANGE, "%s: a cache exceeds 2^31 - 1 pages or slots", what);
+    if (c->dtype != k_cache->dtype) return fail(STG_ERR_INVALID, "%s: k_cache and v_cache differ in dtype", what);
+    for (int d = 0; d < 4; ++d)
+      if (c->shape[d] != k_cache->shape[d])
+        return fail(STG_ERR_INVALID, "%s: k_cache and v_cache differ in shape", what);
+  }
+  return STG_OK;
+}
+
+namespace {
+
+constexpr int kScanThreads = 1024;
+constexpr int kScanPages = 4 * kScanThreads;  // pages per scan workgroup: one 16-byte load a thread
+constexpr int kMoveThreads = 256;
+constexpr int kMoveVecs = 4;  // 16-byte vectors a thread holds in flight
+constexpr int64_t kMoveBytes = int64_t(kMoveThreads) * kMoveVecs * 16;
+
+// Workspace, in int32: a header of 64, `counts` (one per scan workgroup),
+// `first` and `second` (one per page), `rank` (one per row).
+struct PlanSpace {
+  int32_t* header;
+  int32_t* counts;
+  int32_t* first;   // reserve, fork: the free pages; compact: pages that move
+  int32_t* second;  // compact: where they move
+  int32_t* rank;    // reserve, fork: a row's first index into the free pages, or -1
+};
+constexpr int kFree = 0, kNeed = 1, kMoves = 2;  // header slots
+
+int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
+int64_t scan_groups(int64_t pages) { return pages ? (pages + kScanPages - 1) / kScanPages : 1; }
+
+int64_t plan_ints(int64_t pages, int64_t n) {
+  return 64 + round64(scan_groups(pages)) + 2 * round64(pages) + round64(n);
+}
+
+PlanSpace plan_space(void* ws, int64_t pages) {
+  PlanSpace s;
+  s.header = (int32_t*)ws;
+  s.counts = s.header + 64;
+  s.first = s.counts + round64(scan_groups(pages));
+  s.second = s.first + round64(pages);
+  s.rank = s.second + round64(pages);
+  return s;
+}
+
+struct Table {
+  int32_t* data;
+  int64_t stride;
+  int32_t rows, width;
+};
+
+// Every plane of the cache, in bytes.
+struct Planes {
+  char* data;
+  int64_t plane_stride, page_stride, page_bytes;
+  int32_t planes, pages;
+};
+
+__device__ __forceinline__ bool in_range(int32_t i, int32_t n) { return (uint32_t)i < (uint32_t)n; }
+
+// Exclusive prefix sum of v over a workgroup of kScanThreads; *total its sum.
+// `sums` holds one value per wave.
+__device__ __forceinline__ int32_t group_scan(int32_t v, int32_t* sums, int32_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();  // an earlier scan's readers are done with sums
+  if (lane == 63) sums[wave] = x;
+  __syncthreads();
+  int32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kScanThreads / 64; ++w) {
+    before += w < wave ? sums[w] : 0;
+    all += sums[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// Live pages among pages 4 * (first thread index) .. + 3, as bits.
+__device__ __forceinline__ uint32_t live_bits(const int32_t* refs, int64_t at, int32_t pages) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (at + i < pages && refs[at + i] > 0) bits |= 1u << i;
+  return bits;
+}
+
+__global__ __launch_bounds__(kScanThreads) void count_live_kernel(const int32_t* refs, int32_t pages, int32_t* counts) {
+  __shared__ int32_t sums[kScanThreads / 64];
+  const int64_t at = int64_t(blockIdx.x) * kScanPages + threadIdx.x * 4;
+  int32_t total;
+  group_scan(__popc(live_bits(refs, at, pages)), sums, &total);
+  if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+// Sum of counts[0 .. n) by the whole workgroup.
+__device__ __forceinline__ int32_t sum_counts(const int32_t* counts, int32_t n, int32_t* sums) {
+  int32_t v = 0;
+  for (int32_t i = threadIdx.x; i < n; i += kScanThreads) v += counts[i];
+  int32_t total;
+  group_scan(v, sums, &total);
+  return total;
+}
+
+// The free pages in ascending order -> first[], their number -> header.
+__device__ __forceinline__ void list_free(const int32_t* refs, int32_t pages, int32_t groups, const PlanSpace& s,
+                                          int32_t* sums) {
+  const int32_t live_before = groups > 1 ? sum_counts(s.counts, blockIdx.x, sums) : 0;
+  const int64_t at = int64_t(blockIdx.x) * kScanPages + threadIdx.x * 4;
+  const int32_t here = at >= pages ? 0 : (pages - at < 4 ? (int32_t)(pages - at) : 4);
+  const uint32_t free_bits = ~live_bits(refs, at, pages) & ((1u << here) - 1);
+  int32_t total;
+  int32_t rank = blockIdx.x * kScanPages - live_before + group_scan(__popc(free_bits), sums, &total);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (free_bits >> i & 1) s.first[rank++] = (int32_t)(at + i);
+  if (threadIdx.x == 0 && (int32_t)blockIdx.x == groups - 1)
+    s.header[kFree] = blockIdx.x * kScanPages - live_before + total;
+}
+
+// ---- fork -------------------------------------------------------------------
+
+struct Fork {
+  bool ok;      // both rows are in range and differ
+  int32_t len;  // parent's tokens
+  int32_t full; // its full pages
+  int32_t last; // the page to copy, or -1
+};
+
+__device__ __forceinline__ Fork fork_of(const Table& t, const int32_t* lens, int64_t slots, int32_t pages, int32_t p,
+                                        int32_t c) {
+  Fork f{false, 0, 0, -1};
+  if (!in_range(p, t.rows) || !in_range(c, t.rows) || p == c) return f;
+  f.ok = true;
+  const int64_t room = int64_t(t.width) * slots;
+  const int64_t len = lens[p] < 0 ? 0 : lens[p] > room ? room : lens[p];
+  f.len = (int32_t)len;
+  f.full = (int32_t)(len / slots);
+  if (len % slots) {
+    const int32_t e = t.data[p * t.stride + f.full];
+    if (in_range(e, pages)) f.last = e;
+  }
+  return f;
+}
+
+// Workgroups 0 .. groups-1 list the free pages; the last one ranks the forks
+// that need one.
+__global__ __launch_bounds__(kScanThreads) void fork_plan_kernel(Table t, const int32_t* lens, const int32_t* refs,
+                                                                 int32_t pages, int64_t slots, const int32_t* parents,
+                                                                 const int32_t* children, int64_t n, int32_t groups,
+                                                                 PlanSpace s) {
+  __shared__ int32_t sums[kScanThreads / 64];
+  if ((int32_t)blockIdx.x < groups) {
+    list_free(refs, pages, groups, s, sums);
+    return;
+  }
+  int32_t need = 0;
+  for (int64_t i0 = 0; i0 < n; i0 += kScanThreads) {
+    const int64_t i = i0 + threadIdx.x;
+    const bool copies = i < n && fork_of(t, lens, slots, pages, parents[i], children[i]).last >= 0;
+    int32_t total;
+    const int32_t rank = need + group_scan(copies ? 1 : 0, sums, &total);
+    if (i < n) s.rank[i] = copies ? rank : -1;
+    need += total;
+  }
+  if (threadIdx.x == 0) s.header[kNeed] = need;
+}
+
+// Copies `bytes` (at most kMoveBytes) with the whole workgroup: all loads
+// first, then the stores.
+__device__ __forceinline__ void move_bytes(char* dst, const char* src, int64_t bytes) {
+  u32x4 v[kMoveVecs];
+#pragma unroll
+  for (int k = 0; k < kMoveVecs; ++k) {
+    const int64_t o = (int64_t(k) * kMoveThreads + threadIdx.x) * 16;
+    if (o + 16 <= bytes) v[k] = ld16(src + o);
+  }
+#pragma unroll
+  for (int k = 0; k < kMoveVecs; ++k) {
+    const int64_t o = (int64_t(k) * kMoveThreads + threadIdx.x) * 16;
+    if (o + 16 <= bytes) st16(dst + o, v[k]);
+  }
+  const int64_t tail = bytes & 15;
+  if (threadIdx.x < tail) dst[bytes - tail + threadIdx.x] = src[bytes - tail + threadIdx.x];
+}
+
+// Part `part` (kMoveBytes) of page src in plane `plane` to page dst.
+__device__ __forceinline__ void move_part(const Planes& c, int32_t src, int32_t dst, int32_t plane, int64_t part) {
+  const int64_t o = part * kMoveBytes;
+  const int64_t left = c.page_bytes - o;
+  char* base = c.data + plane * c.plane_stride + o;
+  move_bytes(base + dst * c.page_stride, base + src * c.page_stride, left < kMoveBytes ? left : kMoveBytes);
+}
+
+// One workgroup per (fork, plane, part of a page); the first one of a fork
+// also writes the child's row.
+__global__ __launch_bounds__(kMoveThreads) void fork_apply_kernel(Planes cache, Table t, int32_t* lens, int32_t* refs,
+                                                                  int64_t slots, const int32_t* parents,
+                                                                  const int32_t* children, int64_t n, int64_t parts,
+                                                                  int32_t* shortfall, PlanSpace s) {
+  const int32_t free_pages = s.header[kFree];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && shortfall) {
+    const int32_t need = s.header[kNeed];
+    *shortfall = need > free_pages ? need - free_pages : 0;
+  }
+  const int64_t per_fork = cache.planes * parts;
+  const int64_t steps = per_fork ? per_fork : 1;
+  for (int64_t w = blockIdx.x; w < n * steps; w += gridDim.x) {
+    const int64_t i = w / steps, r = w - i * steps;
+    const int32_t p = parents[i], c = children[i];
+    const Fork f = fork_of(t, lens, slots, cache.pages, p, c);
+    if (!f.ok) continue;
+    const int32_t rank = s.rank[i];
+    const int32_t fresh = rank >= 0 && rank < free_pages ? s.first[rank] : -1;
+    if (fresh >= 0 && per_fork) move_part(cache, f.last, fresh, (int32_t)(r / parts), r % parts);
+    if (r) continue;
+    const bool rest = f.len % slots != 0;
+    for (int32_t j = threadIdx.x; j < t.width; j += kMoveThreads) {
+      int32_t e = -1;
+      if (j < f.full) {
+        e = t.data[p * t.stride + j];
+        if (in_range(e, cache.pages))
+          atomicAdd(refs + e, 1);
+        else
+          e = -1;
+      } else if (j == f.full && rest) {
+        e = fresh;
+      }
+      t.data[c * t.stride + j] = e;
+    }
+    if (threadIdx.x == 0) {
+      if (fresh >= 0) refs[fresh] = 1;
+      lens[c] = f.last >= 0 && fresh < 0 ? (int32_t)(f.full * slots) : f.len;
+    }
+  }
+}
+
+// ---- reserve ----------------------------------------------------------------
+
+// Table entries [begin, end) of row b that its next n_new tokens need.
+__device__ __forceinline__ void reserve_range(const Table& t, const int32_t* lens, const int32_t* n_new, int64_t slots,
+                                              int32_t b, int32_t& begin, int32_t& end) {
+  const int64_t room = int64_t(t.width) * slots;
+  const int64_t len = lens[b] < 0 ? 0 : lens[b] > room ? room : lens[b];
+  const int64_t more = n_new[b] < 0 ? 0 : n_new[b];
+  const int64_t to = len + more > room ? room : len + more;
+  begin = (int32_t)(len / slots);
+  end = (int32_t)((to + slots - 1) / slots);
+  if (to <= len) end = begin;
+}
+
+__global__ __launch_bounds__(kScanThreads) void reserve_plan_kernel(Table t, const int32_t* lens, const int32_t* n_new,
+                                                                    const int32_t* refs, int32_t pages, int64_t slots,
+                                                                    int32_t groups, PlanSpace s) {
+  __shared__ int32_t sums[kScanThreads / 64];
+  if ((int32_t)blockIdx.x < groups) {
+    list_free(refs, pages, groups, s, sums);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  for (int32_t b = threadIdx.x >> 6; b < t.rows; b += kScanThreads / 64) {  // a wave counts a row's missing entries
+    int32_t begin, end, missing = 0;
+    reserve_range(t, lens, n_new, slots, b, begin, end);
+    for (int32_t j = begin; j < end; j += 64) {
+      const bool none = j + lane < end && !in_range(t.data[b * t.stride + j + lane], pages);
+      missing += __popcll(__ballot(none));
+    }
+    if (lane == 0) s.rank[b] = missing;
+  }
+  __syncthreads();
+  int32_t need = 0;
+  for (int32_t i0 = 0; i0 < t.rows; i0 += kScanThreads) {
+    const int32_t i = i0 + threadIdx.x;
+    const int32_t mine = i < t.rows ? s.rank[i] : 0;
+    int32_t total;
+    const int32_t before = need + group_scan(mine, sums, &total);
+    if (i < t.rows) s.rank[i] = before;
+    need += total;
+  }
+  if (threadIdx.x == 0) s.header[kNeed] = need;
+}
+
+// A wave per row: its missing entries take the free pages from rank[row] on.
+__global__ __launch_bounds__(256) void reserve_apply_kernel(Table t, const int32_t* lens, const int32_t* n_new,
+                                                            int32_t* refs, int32_t pages, int64_t slots,
+                                                            int32_t* shortfall, PlanSpace s) {
+  const int32_t free_pages = s.header[kFree];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && shortfall) {
+    const int32_t need = s.header[kNeed];
+    *shortfall = need > free_pages ? need - free_pages : 0;
+  }
+  const int lane = threadIdx.x & 63;
+  const int64_t b64 = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (b64 >= t.rows) return;
+  const int32_t b = (int32_t)b64;
+  int32_t begin, end, rank = s.rank[b];
+  reserve_range(t, lens, n_new, slots, b, begin, end);
+  for (int32_t j = begin; j < end; j += 64) {
+    int32_t* e = t.data + b * t.stride + j + lane;
+    const bool none = j + lane < end && !in_range(*e, pages);
+    const uint64_t all = __ballot(none);
+    const int32_t mine = rank + __popcll(all & ((1ull << lane) - 1));
+    if (none && mine < free_pages) {
+      const int32_t page = s.first[mine];
+      *e = page;
+      refs[page] = 1;
+    }
+    rank += __popcll(all);
+  }
+}
+
+// ---- free -------------------------------------------------------------------
+
+// An entry is taken by an exchange, so each is released once however often its
+// row is listed; the counts are integers, so the order of the atomics does not
+// show.
+__global__ __launch_bounds__(256) void free_kernel(Table t, int32_t* lens, int32_t* refs, int32_t pages,
+                                                   const int32_t* rows, int64_t n) {
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const int32_t r = rows[i];
+    if (!in_range(r, t.rows)) continue;
+    for (int32_t j = threadIdx.x; j < t.width; j += 256) {
+      int32_t* e = t.data + r * t.stride + j;
+      if (*e == -1) continue;
+      const int32_t page = atomicExch(e, -1);
+      if (in_range(page, pages)) atomicSub(refs + page, 1);
+    }
+    if (threadIdx.x == 0) lens[r] = 0;
+  }
+}
+
+// ---- copy -------------------------------------------------------------------
+
+__global__ __launch_bounds__(kMoveThreads) void copy_kernel(Planes cache, const int32_t* src, const int32_t* dst,
+                                                            int64_t n, int64_t parts) {
+  const int64_t steps = cache.planes * parts;
+  for (int64_t w = blockIdx.x; w < n * steps; w += gridDim.x) {
+    const int64_t i = w / steps, r = w - i * steps;
+    const int32_t a = src[i], b = dst[i];
+    if (!in_range(a, cache.pages) || !in_range(b, cache.pages)) continue;
+    move_part(cache, a, b, (int32_t)(r / parts), r % parts);
+  }
+}
+
+// ---- compact ----------------------------------------------------------------
+
+// With L live pages and live(p) the live pages below p: a live page p >= L is
+// the (live(p) - live(L))-th that moves, a free page p < L the (p - live(p))-th
+// place.  remap holds a moving page's rank r as -2 - r until the apply.
+__global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(const int32_t* refs, int32_t pages, int32_t groups,
+                                                                    int32_t* remap, PlanSpace s) {
+  __shared__ int32_t sums[kScanThreads / 64];
+  __shared__ int32_t border;
+  int32_t live_before = 0, total, live, at_border;
+  const int64_t at = int64_t(blockIdx.x) * kScanPages + threadIdx.x * 4;
+  const uint32_t bits = live_bits(refs, at, pages);
+  int32_t below = group_scan(__popc(bits), sums, &total);
+  if (groups > 1) {
+    live_before = sum_counts(s.counts, blockIdx.x, sums);
+    live = sum_counts(s.counts, groups, sums);
+    const int32_t g = live / kScanPages < groups ? live / kScanPages : groups - 1;  // the group that L lies in
+    const int64_t from = int64_t(g) * kScanPages + threadIdx.x * 4;
+    const int64_t keep = live - from;  // pages of these four below L
+    uint32_t b = live_bits(refs, from, pages);
+    b &= keep <= 0 ? 0u : keep >= 4 ? 0xFu : (1u << keep) - 1;
+    int32_t inside;
+    group_scan(__popc(b), sums, &inside);
+    at_border = inside + sum_counts(s.counts, g, sums);
+  } else {
+    live = total;
+    // the thread whose pages hold L, or the last one where L is past them all
+    if (at <= live && (live < at + 4 || threadIdx.x == kScanThreads - 1)) {
+      const int64_t keep = live - at;
+      border = below + __popc(bits & (keep >= 4 ? 0xFu : (1u << keep) - 1));
+    }
+    __syncthreads();
+    at_border = border;
+  }
+  below += live_before;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t p = at + i;
+    if (p < pages) {
+      const bool is_live = bits >> i & 1;
+      int32_t to = is_live ? (int32_t)p : -1;
+      if (is_live && p >= live) {
+        const int32_t r = below - at_border;
+        s.first[r] = (int32_t)p;
+        to = -2 - r;
+      } else if (!is_live && p < live) {
+        s.second[p - below] = (int32_t)p;
+      }
+      remap[p] = to;
+      below += is_live ? 1 : 0;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) s.header[kMoves] = live - at_border;
+}
+
+__global__ __launch_bounds__(kMoveThreads) void compact_apply_kernel(Planes cache, Table t, int32_t* refs,
+                                                                     int32_t* remap, int64_t parts, PlanSpace s) {
+  const int32_t moves = s.header[kMoves];
+  const int64_t self = int64_t(blockIdx.x) * kMoveThreads + threadIdx.x;
+  const int64_t all = int64_t(gridDim.x) * kMoveThreads;
+  for (int64_t i = self; i < int64_t(t.rows) * t.width; i += all) {
+    const int64_t b = i / t.width;
+    int32_t* e = t.data + b * t.stride + (i - b * t.width);
+    if (!in_range(*e, cache.pages)) continue;
+    // a moving page's entry of remap is its rank, or already its new number:
+    // both name the same page
+    const int32_t r = __hip_atomic_load(remap + *e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (r <= -2) *e = s.second[-2 - r];
+    else if (r >= 0 && r != *e) *e = r;
+  }
+  for (int64_t i = self; i < moves; i += all) {
+    const int32_t a = s.first[i], b = s.second[i];
+    refs[b] = refs[a];
+    refs[a] = 0;
+    __hip_atomic_store(remap + a, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  const int64_t steps = cache.planes * parts;
+  for (int64_t w = blockIdx.x; w < moves * steps; w += gridDim.x) {
+    const int64_t i = w / steps, r = w - i * steps;
+    move_part(cache, s.first[i], s.second[i], (int32_t)(r / parts), r % parts);
+  }
+}
+
+// ---- host -------------------------------------------------------------------
+
+constexpr int64_t kMoveGrid = 4096;  // workgroups of a copy: 16 per CU, each loops
+
+int check_cache(const char* what, const stg_tensor* c) {
+  if (int rc = check_tensor(c, "cache")) return rc;
+  if (c->rank != 3 || (c->shape[2] > 1 && c->stride[2] != 1))
+    return fail(STG_ERR_INVALID, "%s: cache must be (planes, pages, elements) with unit element stride", what);
+  if (c->shape[0] > kMaxCount || c->shape[1] > kMaxCount)
+    return fail(STG_ERR_RANGE, "%s: cache exceeds 2^31 - 1 planes or pages", what);
+  if (c->shape[1] > 1 && c->stride[1] < c->shape[2]) return fail(STG_ERR_INVALID, "%s: pages overlap", what);
+  return STG_OK;
+}
+
+// A row's length is an int32 and a table row holds width * slots tokens; the
+// product is kept far from overflow.
+int check_slots(const char* what, int64_t slots) {
+  if (slots < 1) return fail(STG_ERR_INVALID, "%s: slots must be >= 1", what);
+  if (slots > kMaxCount) return fail(STG_ERR_RANGE, "%s: slots exceeds 2^31 - 1", what);
+  return STG_OK;
+}
+
+int check_space(const char* what, const void* ws, int64_t bytes, int64_t pages, int64_t n) {
+  const int64_t need = pages_workspace(pages, n);
+  if (need < 0) return (int)-need;
+  if (!ws || bytes < need)
+    return fail(STG_ERR_INVALID, "%s: needs a workspace of %lld bytes (pages_workspace)", what, (long long)need);
+  if ((uintptr_t)ws & 255) return fail(STG_ERR_INVALID, "%s: workspace must be 256-byte aligned", what);
+  return STG_OK;
+}
+
+Table table_of(const stg_tensor* t) {
+  return Table{(int32_t*)t->data, t->stride[0], (int32_t)t->shape[0], (int32_t)t->shape[1]};
+}
+
+Planes planes_of(const stg_tensor* c) {
+  const int64_t es = dtype_size(c->dtype);
+  return Planes{(char*)c->data, c->stride[0] * es, c->stride[1] * es, c->shape[2] * es, (int32_t)c->shape[0],
+                (int32_t)c->shape[1]};
+}
+
+int64_t parts_of(const Planes& c) { return (c.page_bytes + kMoveBytes - 1) / kMoveBytes; }
+
+uint32_t grid_of(int64_t items) { return (uint32_t)(items < 1 ? 1 : items > kMoveGrid ? kMoveGrid : items); }
+
+// items = a * b * c of a looping grid, saturated
+int64_t product(int64_t a, int64_t b, int64_t c) {
+  int64_t v;
+  if (__builtin_mul_overflow(a, b, &v) || __builtin_mul_overflow(v, c, &v)) return INT64_MAX;
+  return v;
+}
+
+int count_if_many(const char* name, const int32_t* refs, int32_t pages, int32_t groups, const PlanSpace& s,
+                  hipStream_t st) {
+  if (groups < 2) return STG_OK;
+  launch_kernel(name, count_live_kernel, dim3(groups), dim3(kScanThreads), 0, st, refs, pages, s.counts);
+  return check_launch(name);
+}
+
+}  // namespace
+}  // namespace stg
+
+using namespace stg;
+
+extern "C" int64_t pages_workspace(int64_t n_pages, int64_t n) {
+  clear_error();
+  if (n_pages < 0 || n < 0) return -fail(STG_ERR_INVALID, "pages_workspace: negative count");
+  if (n_pages > kMaxCount || n > kMaxCount) return -fail(STG_ERR_RANGE, "pages_workspace: a count exceeds 2^31 - 1");
+  return 4 * plan_ints(n_pages, n);
+}
+
+extern "C" int pages_copy(const stg_tensor* cache, const int32_t* src, const int32_t* dst, int64_t n, void* stream) {
+  clear_error();
+  if (int rc = check_cache("pages_copy", cache)) return rc;
+  if (n < 0) return fail(STG_ERR_INVALID, "pages_copy: negative count");
+  if (n > kMaxCount) return fail(STG_ERR_RANGE, "pages_copy: count exceeds 2^31 - 1");
+  if (n > 0 && (!src || !dst)) return fail(STG_ERR_INVALID, "pages_copy: null src or dst");
+  const Planes c = planes_of(cache);
+  const int64_t parts = parts_of(c), items = product(n, c.planes, parts);
+  if (items == INT64_MAX) return fail(STG_ERR_RANGE, "pages_copy: too many pages");
+  if (!items || !c.pages) return STG_OK;
+  launch_kernel("pages_copy", copy_kernel, dim3(grid_of(items)), dim3(kMoveThreads), 0, as_stream(stream), c, src, dst,
+                n, parts);
+  return check_launch("pages_copy");
+}
+
+extern "C" int pages_reserve(const stg_tensor* page_table, const int32_t* seq_lens, const int32_t* n_new, int32_t* refs,
+                             int64_t n_pages, int64_t slots, int32_t* shortfall, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* what = "pages_reserve";
+  if (int rc = check_page_table(what, page_table)) return rc;
+  if (int rc = check_slots(what, slots)) return rc;
+  if (int rc = check_space(what, workspace, workspace_bytes, n_pages, page_table->shape[0])) return rc;
+  const Table t = table_of(page_table);
+  if ((t.rows && (!seq_lens || !n_new)) || (n_pages && !refs))
+    return fail(STG_ERR_INVALID, "%s: null seq_lens, n_new or refs", what);
+  const PlanSpace s = plan_space(workspace, n_pages);
+  const int32_t groups = (int32_t)scan_groups(n_pages);
+  const hipStream_t st = as_stream(stream);
+  if (int rc = count_if_many("pages_reserve/count", refs, (int32_t)n_pages, groups, s, st)) return rc;
+  launch_kernel("pages_reserve/plan", reserve_plan_kernel, dim3(groups + 1), dim3(kScanThreads), 0, st, t, seq_lens,
+                n_new, refs, (int32_t)n_pages, slots, groups, s);
+  if (int rc = check_launch("pages_reserve/plan")) return rc;
+  launch_kernel("pages_reserve", reserve_apply_kernel, dim3(t.rows ? (t.rows + 3) / 4 : 1), dim3(256), 0, st, t,
+                seq_lens, n_new, refs, (int32_t)n_pages, slots, shortfall, s);
+  return check_launch("pages_reserve");
+}
+
+extern "C" int pages_fork(const stg_tensor* cache, const stg_tensor* page_table, int32_t* seq_lens, int32_t* refs,
+                          int64_t slots, const int32_t* parents, const int32_t* children, int64_t n,
+                          int32_t* shortfall, void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* what = "pages_fork";
+  if (int rc = check_cache(what, cache)) return rc;
+  if (int rc = check_page_table(what, page_table)) return rc;
+  if (int rc = check_slots(what, slots)) return rc;
+  const Planes c = planes_of(cache);
+  const Table t = table_of(page_table);
+  if (int rc = check_space(what, workspace, workspace_bytes, c.pages, n)) return rc;
+  if ((t.rows && !seq_lens) || (c.pages && !refs) || (n && (!parents || !children)))
+    return fail(STG_ERR_INVALID, "%s: null seq_lens, refs, parents or children", what);
+  const int64_t parts = parts_of(c), per = product(c.planes, parts, 1), items = product(n, per ? per : 1, 1);
+  if (items == INT64_MAX) return fail(STG_ERR_RANGE, "%s: too many pages", what);
+  const PlanSpace s = plan_space(workspace, c.pages);
+  const int32_t groups = (int32_t)scan_groups(c.pages);
+  const hipStream_t st = as_stream(stream);
+  if (int rc = count_if_many("pages_fork/count", refs, c.pages, groups, s, st)) return rc;
+  launch_kernel("pages_fork/plan", fork_plan_kernel, dim3(groups + 1), dim3(kScanThreads), 0, st, t,
+                (const int32_t*)seq_lens, (const int32_t*)refs, c.pages, slots, parents, children, n, groups, s);
+  if (int rc = check_launch("pages_fork/plan")) return rc;
+  launch_kernel("pages_fork", fork_apply_kernel, dim3(grid_of(items)), dim3(kMoveThreads), 0, st, c, t, seq_lens, refs,
+                slots, parents, children, n, parts, shortfall, s);
+  return check_launch("pages_fork");
+}
+
+extern "C" int pages_free(const stg_tensor* page_table, int32_t* seq_lens, int32_t* refs, int64_t n_pages,
+                          const int32_t* rows, int64_t n, void* stream) {
+  clear_error();
+  const char* what = "pages_free";
+  if (int rc = check_page_table(what, page_table)) return rc;
+  if (n_pages < 0 || n < 0) return fail(STG_ERR_INVALID, "%s: negative count", what);
+  if (n_pages > kMaxCount || n > kMaxCount) return fail(STG_ERR_RANGE, "%s: a count exceeds 2^31 - 1", what);
+  const Table t = table_of(page_table);
+  if ((t.rows && !seq_lens) || (n_pages && !refs) || (n && !rows))
+    return fail(STG_ERR_INVALID, "%s: null seq_lens, refs or rows", what);
+  if (!n || !t.rows) return STG_OK;
+  launch_kernel("pages_free", free_kernel, dim3(grid_of(n)), dim3(256), 0, as_stream(stream), t, seq_lens, refs,
+                (int32_t)n_pages, rows, n);
+  return check_launch("pages_free");
+}
+
+extern "C" int pages_compact(const stg_tensor* cache, const stg_tensor* page_table, int32_t* refs, int32_t* remap,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* what = "pages_compact";
+  if (int rc = check_cache(what, cache)) return rc;
+  if (int rc = check_page_table(what, page_table)) return rc;
+  const Planes c = planes_of(cache);
+  const Table t = table_of(page_table);
+  if (int rc = check_space(what, workspace, workspace_bytes, c.pages, 0)) return rc;
+  if (c.pages && (!refs || !remap)) return fail(STG_ERR_INVALID, "%s: null refs or remap", what);
+  const int64_t parts = parts_of(c), items = product(c.pages / 2, c.planes, parts);
+  if (items == INT64_MAX) return fail(STG_ERR_RANGE, "%s: too many pages", what);
+  if (!c.pages) return STG_OK;
+  const PlanSpace s = plan_space(workspace, c.pages);
+  const int32_t groups = (int32_t)scan_groups(c.pages);
+  const hipStream_t st = as_stream(stream);
+  if (int rc = count_if_many("pages_compact/count", refs, c.pages, groups, s, st)) return rc;
+  launch_kernel("pages_compact/plan", compact_plan_kernel, dim3(groups), dim3(kScanThreads), 0, st,
+                (const int32_t*)refs, c.pages, groups, remap, s);
+  if (int rc = check_launch("pages_compact/plan")) return rc;
+  launch_kernel("pages_compact", compact_apply_kernel, dim3((uint32_t)kMoveGrid), dim3(kMoveThreads), 0, st, c, t, refs,
+                remap, parts, s);
+  return check_launch("pages_compact");
+}

@@ -202,6 +202,13 @@ struct GemmNames {
 int gemm_bf16(const GemmNames& names, const void* A, int64_t lda, const void* B, int64_t ldb, const float* acc,
               int64_t ldacc, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, int32_t c_dtype, hipStream_t s);
 
+// Checks shared by the operations on a paged key-value cache (pages.hip):
+// k_cache and v_cache (pages, slots, heads, depth) of one shape and dtype, bf16,
+// f16 or u8, unit last stride; page_table (rows, width) int32, unit last stride.
+int check_page_table(const char* what, const stg_tensor* page_table);
+int check_paged_cache(const char* what, const stg_tensor* k_cache, const stg_tensor* v_cache,
+                      const stg_tensor* page_table);
+
 // Block-scaled GEMM for the operand pairs, scale formats and blocks the
 // scaled MFMA does not take (gemm_scaled_general.hip); arguments as
 // gemm_scaled's, already checked by it.  With a workspace of at least
