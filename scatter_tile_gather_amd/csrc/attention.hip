@@ -35,8 +35,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kBlock = 32;    // tokens of a wave's iteration
-constexpr int kSpan = 1024;   // tokens whose addresses are in LDS at a time
-constexpr float kRaise = 8.f; // log2 of how far a score may exceed the running maximum
+constexpr int kSpan = 128;    // tokens of a wave whose addresses are in LDS at a time
+constexpr int kSpanBlocks = kSpan / kBlock;
 constexpr int kQueries = 16;  // query heads of a workgroup
 
 struct Args {
@@ -56,17 +56,38 @@ struct Args {
   float2* stat;  // (rows, q_heads, splits): maximum (log2) and sum
   float scale_log2;
   int32_t rows, width, pages, slots;
-  int32_t heads, group, tiles, depth, splits;
+  int32_t heads, group, tiles, depth, splits, share;  // share: tokens of a split
   int64_t window;
 };
 
+// p = 2^(x - m) is kept in [0, 2^kRaise]: m is set to the largest x minus
+// kLift, and again once an x exceeds it by more than kRaise.  f16's smallest
+// step is 2^-24, and a long row's many small terms must not vanish below it
+// beside a large one, so its p are lifted towards its largest number; bf16 has
+// fp32's exponents.
+//
+// split: two p as two pairs of terms, p = hi + lo up to 2^-17 of it (f16: 2^-20
+// of it, or 2^-24).  hi is cut, not rounded, so that lo is not negative, and lo
+// is at least the type's least (far below what it could change): an infinite
+// value times hi plus lo is then what it is times p, where a lo of 0 would
+// make it NaN.
+
 struct BF16 {
+  static constexpr float kLift = 0.f, kRaise = 8.f;
   typedef __bf16 x8 __attribute__((ext_vector_type(8)));
   static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }
   static __device__ __forceinline__ uint32_t put(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
-  static __device__ __forceinline__ float get(uint32_t b) { return __uint_as_float(b << 16); }
+  static __device__ __forceinline__ void split(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+    hi = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+    const f2 rest = {fmaxf(p0 - __uint_as_float(b0 & 0xFFFF0000u), 0x1p-100f),
+                     fmaxf(p1 - __uint_as_float(b1 & 0xFFFF0000u), 0x1p-100f)};
+    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, b2));
+  }
   // two e4m3 codes (the low or the high half of w); bf16 holds every code exactly
   template <bool HIGH>
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
@@ -74,40 +95,28 @@ struct BF16 {
   }
 };
 struct F16 {
+  static constexpr float kLift = 11.f, kRaise = 15.f;
   typedef _Float16 x8 __attribute__((ext_vector_type(8)));
   static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }
   static __device__ __forceinline__ uint32_t put(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
-  static __device__ __forceinline__ float get(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
+  static __device__ __forceinline__ void split(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+    const auto h = __builtin_amdgcn_cvt_pkrtz(p0, p1);
+    hi = __builtin_bit_cast(uint32_t, h);
+    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(fmaxf(p0 - (float)h[0], 0x1p-24f),
+                                                                 fmaxf(p1 - (float)h[1], 0x1p-24f)));
+  }
   template <bool HIGH>
   static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, HIGH));
   }
 };
 
-// Eight elements moved down by n (0 .. 8) places of 16 bits, zeros above.
-__device__ __forceinline__ u32x4 drop16(u32x4 v, int n) {
-  uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
-  if (n >= 8) {
-    lo = hi = 0;
-  } else if (n >= 4) {
-    lo = hi >> (16 * (n - 4));
-    hi = 0;
-  } else if (n > 0) {
-    lo = lo >> (16 * n) | hi << (64 - 16 * n);
-    hi >>= 16 * n;
-  }
-  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-
 // The tokens of row b that are attended, [begin, end), and this split's share.
 struct Range {
   int32_t begin, end;
 };
-__host__ __device__ __forceinline__ int64_t split_tokens(int64_t n, int32_t splits) {
-  return ((n + splits - 1) / splits + kBlock - 1) / kBlock * kBlock;
-}
 __device__ __forceinline__ Range attended(const Args& a, int32_t b) {
   const int64_t room = int64_t(a.width) * a.slots;
   const int64_t len = a.lens[b] < 0 ? 0 : a.lens[b] > room ? room : a.lens[b];
@@ -115,47 +124,79 @@ __device__ __forceinline__ Range attended(const Args& a, int32_t b) {
   return Range{(int32_t)begin, (int32_t)len};
 }
 
-// DS: depth in steps of 32 (rounded up); E4M3: the caches hold e4m3 codes.
-template <class T, int DS, bool E4M3>
+// Tokens of a split of this row: the host's, or more where the row is longer
+// than the host was told.
+__device__ __forceinline__ int share_of(const Args& a, const Range& all) {
+  const int n = all.end - all.begin;
+  if (n <= int64_t(a.share) * a.splits) return a.share;
+  return (n - 1) / a.splits + 1;
+}
+
+// Orders a wave's LDS accesses against each other: the LDS unit runs one
+// wave's instructions in order, so only the compiler has to be held.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ void put_words(uint32_t* w, u32x4 x) { w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3]; }
+__device__ __forceinline__ void put_words(uint32_t* w, u32x2 x) { w[0] = x[0], w[1] = x[1]; }
+template <class V>
+__device__ __forceinline__ V load_as(const char* p) {
+  V v;
+  __builtin_memcpy(&v, p, sizeof(V));
+  return v;
+}
+
+// DS: depth in steps of 32 (rounded up); E4M3: the caches hold e4m3 codes;
+// RAGGED: depth is not 32 DS.
+template <class T, int DS, bool E4M3, bool RAGGED>
 struct Geometry {
-  static constexpr int kSteps = DS;
-  // a lane's share of a value row, in dimensions: chunks of 8 over 128
+  // ---- queries and keys: a lane of group grp holds 8 dimensions of each step
+  // of 32.  Which ones is free as long as both sides agree: 8 codes are only 8
+  // bytes, so pairs of steps take 16 codes in a row with one load.
+  static constexpr bool kPairs = E4M3 && !RAGGED;
+  static constexpr int kWords = E4M3 ? 2 : 4;  // 32-bit words of 8 elements
+  static __device__ __forceinline__ int dim(int step, int grp) {
+    if (kPairs && (step | 1) < DS) return 64 * (step >> 1) + 16 * grp + 8 * (step & 1);
+    return 32 * step + 8 * grp;
+  }
+  // first dimension that is read: a chunk that would pass the row's end is
+  // read further down, so every load stays inside the row, and what it has
+  // below dim() is masked
+  static __device__ __forceinline__ int from(int step, int grp, int depth) {
+    const int d = dim(step, grp);
+    return RAGGED && d > depth - 8 ? depth - 8 : d;
+  }
+  static __device__ __forceinline__ u32x4 mask(int step, int grp, int depth) {
+    const int over = dim(step, grp) - from(step, grp, depth);
+    u32x4 m;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m[w] = (2 * w >= over ? 0xFFFFu : 0u) | (2 * w + 1 >= over ? 0xFFFF0000u : 0u);
+    return m;
+  }
+  // steps that can pass the row's end (depth > 32 (DS - 2) for every DS used)
+  static __device__ __forceinline__ constexpr bool masked(int step) { return RAGGED && step >= DS - 2; }
+
+  // ---- values: a lane's share of a row, in dimensions: chunks of 8 over 128
   // dimensions, one chunk of 4 for a rest of 64
   static constexpr int kDims = DS <= 2 ? 4 : DS <= 4 ? 8 : DS <= 6 ? 12 : 16;
   static constexpr int kEights = kDims / 8;
   static constexpr int kFours = kDims % 8 / 4;
+  static constexpr int kValueWords = kDims * (E4M3 ? 1 : 2) / 4;
+  // every lane's chunks lie inside the row
+  static constexpr bool kExact = !RAGGED && 16 * kDims == 32 * DS;
 };
 
-// 8 dimensions of a K or V row as 16-bit elements.
 template <class T, bool E4M3>
-struct Raw8 {
-  using type = std::conditional_t<E4M3, u32x2, u32x4>;
-  static __device__ __forceinline__ type load(const char* p) {
-    type v;
-    __builtin_memcpy(&v, p, sizeof(v));
-    return v;
-  }
-  static __device__ __forceinline__ u32x4 wide(type v) {
-    if constexpr (E4M3)
-      return u32x4{T::template from_e4m3<false>(v[0]), T::template from_e4m3<true>(v[0]),
-                   T::template from_e4m3<false>(v[1]), T::template from_e4m3<true>(v[1])};
-    else
-      return v;
-  }
-};
-template <class T, bool E4M3>
-struct Raw4 {
-  using type = std::conditional_t<E4M3, uint32_t, u32x2>;
-  static __device__ __forceinline__ type load(const char* p) {
-    type v;
-    __builtin_memcpy(&v, p, sizeof(v));
-    return v;
-  }
-  static __device__ __forceinline__ u32x2 wide(type v) {
-    if constexpr (E4M3) return u32x2{T::template from_e4m3<false>(v), T::template from_e4m3<true>(v)};
-    else return v;
-  }
-};
+__device__ __forceinline__ u32x4 wide8(const uint32_t* w) {
+  if constexpr (E4M3)
+    return u32x4{T::template from_e4m3<false>(w[0]), T::template from_e4m3<true>(w[0]),
+                 T::template from_e4m3<false>(w[1]), T::template from_e4m3<true>(w[1])};
+  else
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
 
 // Elements 2w and 2w+1 of eight rows -> the two operands that hold one
 // dimension of the eight tokens each.
@@ -167,22 +208,20 @@ __device__ __forceinline__ void transpose_pair(const uint32_t (&r)[8], u32x4& ev
   }
 }
 
-template <class T, int DS, bool E4M3>
-__global__ __launch_bounds__(kThreads) void paged_attention_kernel(Args a) {
-  using G = Geometry<T, DS, E4M3>;
-  using R8 = Raw8<T, E4M3>;
-  using R4 = Raw4<T, E4M3>;
+template <class T, int DS, bool E4M3, bool RAGGED>
+__global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged_attention_kernel(Args a) {
+  using G = Geometry<T, DS, E4M3, RAGGED>;
   constexpr int kElem = E4M3 ? 1 : 2;
-  // token addresses during the loop, the waves' sums after it
+  // token addresses during the loop (two spans a wave), the waves' sums after it
   __shared__ union {
     struct {
-      int64_t k[kSpan], v[kSpan];
+      int64_t k[kWaves][2][kSpan], v[kWaves][2][kSpan];
     } at;
     float sums[kWaves][kQueries][128];
   } lds;
   __shared__ float2 stats[kWaves][kQueries];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, grp = lane >> 4;
   uint32_t id = blockIdx.x;
   const int h = id % a.heads;
@@ -193,179 +232,215 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(Args a) {
   const int b = id / a.splits;
 
   const Range all = attended(a, b);
-  const int64_t share = split_tokens(all.end - all.begin, a.splits);
-  const int64_t begin = all.begin + split * share;
-  const int64_t end = begin + share < all.end ? begin + share : all.end;
-  if (begin >= end && split > 0) return;  // the join knows which parts exist
+  const int share = share_of(a, all);
+  const int64_t part_begin = all.begin + int64_t(split) * share;
+  if (part_begin >= all.end && split > 0) return;  // the join knows which parts exist
+  const int part_tokens = all.end - part_begin < share ? (int)(all.end - part_begin) : share;
+  // a wave takes a run of tokens, whole blocks but for the last
+  const int run = (part_tokens + kWaves * kBlock - 1) / (kWaves * kBlock) * kBlock;
+  const int left = part_tokens - wave * run;
+  const int n = left < 0 ? 0 : left < run ? left : run;
+  const uint32_t begin = (uint32_t)part_begin + wave * run;
+  const int blocks = (n + kBlock - 1) / kBlock;
 
-  // queries: operand column `col`, dimensions 8 grp + 32 step ..
+  // queries: operand column `col`
   const int head0 = h * a.group + tile * kQueries;
   const int queries = a.group - tile * kQueries < kQueries ? a.group - tile * kQueries : kQueries;
-  u32x4 qf[G::kSteps];
+  u32x4 qf[DS];
   {
     const char* q = a.q + b * a.q_row + (head0 + (col < queries ? col : 0)) * a.q_head;
 #pragma unroll
-    for (int s = 0; s < G::kSteps; ++s) {
-      const int d = 8 * grp + 32 * s;
-      const int from = d < a.depth - 8 ? d : a.depth - 8;
-      u32x4 x;
-      __builtin_memcpy(&x, q + 2 * from, 16);
-      qf[s] = col < queries ? drop16(x, d - from < 8 ? d - from : 8) : u32x4{0, 0, 0, 0};
+    for (int s = 0; s < DS; ++s) {
+      const u32x4 x = ld16(q + 2 * G::from(s, grp, a.depth));
+      qf[s] = col < queries ? x & G::mask(s, grp, a.depth) : u32x4{0, 0, 0, 0};
     }
   }
   const float c = a.scale_log2 * (a.k_scale ? a.k_scale[h] : 1.f);
-  const char* kbase = a.k + h * a.k_head;
-  const char* vbase = a.v + h * a.v_head;
-  // where this lane's K chunks and V chunks begin; a chunk that would pass the
-  // row's end is read further down, so every load stays inside the row
-  int kd[G::kSteps];
-#pragma unroll
-  for (int s = 0; s < G::kSteps; ++s) {
-    const int d = 8 * grp + 32 * s;
-    kd[s] = d < a.depth - 8 ? d : a.depth - 8;
-  }
-  int vd8[G::kEights ? G::kEights : 1], vd4 = 0;
-#pragma unroll
-  for (int i = 0; i < G::kEights; ++i) {
+  const char* kbase = a.k + h * a.k_head + (RAGGED ? 0 : G::dim(0, grp) * kElem);
+  const char* vbase = a.v + h * a.v_head + (G::kExact ? (G::kEights ? 8 : 4) * col * kElem : 0);
+  // where this lane's chunks begin, from those bases
+  const auto key_at = [&](int s) {
+    return (RAGGED ? G::from(s, grp, a.depth) : G::dim(s, grp) - G::dim(0, grp)) * kElem;
+  };
+  const auto value8_at = [&](int i) {
     const int d = 128 * i + 8 * col;
-    vd8[i] = d < a.depth - 8 ? d : a.depth - 8;
-  }
-  if constexpr (G::kFours > 0) {
+    return (G::kExact ? 128 * i : d < a.depth - 8 ? d : a.depth - 8) * kElem;
+  };
+  const auto value4_at = [&]() {
     const int d = 128 * G::kEights + 4 * col;
-    vd4 = d < a.depth - 4 ? d : a.depth - 4;
-  }
-  const bool ragged = a.depth != 32 * DS;
+    return (G::kExact ? (G::kEights ? d - 8 * col : 0) : d < a.depth - 4 ? d : a.depth - 4) * kElem;
+  };
 
-  f32x4 o[G::kDims];
+  // A span's addresses: its pages are loaded a span ahead, its offsets go to
+  // LDS when the loop reaches it.  A token without a page has offset 0, which
+  // may be read, and a zero in `there`.
+  int32_t page[2];
+  const auto fetch = [&](int span) {
 #pragma unroll
-  for (int e = 0; e < G::kDims; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, sum = 0.f;
-
-  for (int64_t s0 = begin; s0 < end; s0 += kSpan) {
-    const int n = end - s0 < kSpan ? (int)(end - s0) : kSpan;
-    const int blocks = (n + kBlock - 1) / kBlock;
-    __syncthreads();
-    for (int i = threadIdx.x; i < blocks * kBlock; i += kThreads) {
-      int64_t ka = -1, va = -1;
-      if (i < n) {
-        const int32_t j = (int32_t)(s0 + i), entry = j / a.slots;
-        const int32_t page = a.table[b * a.table_stride + entry];
-        if ((uint32_t)page < (uint32_t)a.pages) {
-          const int64_t slot = j - entry * a.slots;
-          ka = page * a.k_page + slot * a.k_slot;
-          va = page * a.v_page + slot * a.v_slot;
-        }
-      }
-      lds.at.k[i] = ka;
-      lds.at.v[i] = va;
+    for (int t = 0; t < 2; ++t) {
+      const int i = span * kSpan + 64 * t + lane;
+      page[t] = i < n ? a.table[b * a.table_stride + (begin + i) / (uint32_t)a.slots] : -1;
     }
-    __syncthreads();
-    for (int blk = wave; blk < blocks; blk += kWaves) {
-      const int i0 = blk * kBlock;
-      // scores of tokens 16 t + 4 grp + r for query `col`
-      f32x4 s[2];
+  };
+  uint64_t there[2];
+  const auto place = [&](int span) {
+    int64_t* k = lds.at.k[wave][span & 1];
+    int64_t* v = lds.at.v[wave][span & 1];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int64_t at = lds.at.k[i0 + 16 * t + col];
-        const char* row = kbase + (at < 0 ? 0 : at);
-        u32x4 kf[G::kSteps];
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t j = begin + span * kSpan + 64 * t + lane;
+      const int64_t slot = j % (uint32_t)a.slots;
+      const bool ok = (uint32_t)page[t] < (uint32_t)a.pages;
+      k[64 * t + lane] = ok ? page[t] * a.k_page + slot * a.k_slot : 0;
+      v[64 * t + lane] = ok ? page[t] * a.v_page + slot * a.v_slot : 0;
+      there[t] = __ballot(ok);
+    }
+    wave_sync();
+  };
+
+  using key_vec = std::conditional_t<E4M3, u32x2, u32x4>;  // 8 elements
+  uint32_t kw[2][DS * G::kWords];   // keys of tokens col and 16 + col
+  uint32_t vw[8][G::kValueWords];   // values of tokens 4 grp + i, 12 + 4 grp + i (i >= 4)
+  const auto load_keys = [&](int blk) {
+    const int64_t* k = &lds.at.k[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
 #pragma unroll
-        for (int st = 0; st < G::kSteps; ++st) kf[st] = R8::wide(R8::load(row + kd[st] * kElem));
-        if (ragged) {
+    for (int t = 0; t < 2; ++t) {
+      const char* row = kbase + k[16 * t + col];
 #pragma unroll
-          for (int st = 0; st < G::kSteps; ++st) {
-            const int over = 8 * grp + 32 * st - kd[st];
-            kf[st] = drop16(kf[st], over < 8 ? over : 8);
-          }
+      for (int s = 0; s < DS; ++s) {
+        uint32_t* w = kw[t] + s * G::kWords;
+        if (G::kPairs && (s | 1) < DS) {
+          if (s & 1) continue;  // came with the step before
+          put_words(w, load_as<u32x4>(row + key_at(s)));
+        } else {
+          put_words(w, load_as<key_vec>(row + key_at(s)));
         }
-        s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int st = 0; st < G::kSteps; ++st) s[t] = T::mma(kf[st], qf[st], s[t]);
       }
-      int64_t va[8];
+    }
+  };
+  const auto load_values = [&](int blk) {
+    const int64_t* v = &lds.at.v[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) va[i] = lds.at.v[i0 + 16 * (i >> 2) + 4 * grp + (i & 3)];
-      float x[8], top = -INFINITY;
+    for (int i = 0; i < 8; ++i) {
+      const char* row = vbase + v[16 * (i >> 2) + 4 * grp + (i & 3)];
+      uint32_t* w = vw[i];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = va[i] < 0 ? -INFINITY : s[i >> 2][i & 3] * c;
-        top = fmaxf(top, x[i]);
-      }
-      if (__ballot(top > m + kRaise)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float to = fmaxf(m, top);
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
-        m = to;
-        sum *= f;
-        float fr[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) fr[r] = __shfl(f, 4 * grp + r);
-#pragma unroll
-        for (int e = 0; e < G::kDims; ++e)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[e][r] *= fr[r];
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      u32x4 hi, lo;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p0 = __builtin_amdgcn_exp2f(x[2 * i] - base), p1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - base);
-        sum += p0 + p1;
-        const uint32_t h0 = T::put(p0), h1 = T::put(p1);
-        hi[i] = h0 | h1 << 16;
-        lo[i] = T::put(p0 - T::get(h0)) | T::put(p1 - T::get(h1)) << 16;
-      }
-      bool holes = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) holes |= va[i] < 0;
-      const bool any_hole = __ballot(holes) != 0;
-#pragma unroll
-      for (int g8 = 0; g8 < G::kEights; ++g8) {
-        u32x4 rows[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rows[i] = R8::wide(R8::load(vbase + (va[i] < 0 ? 0 : va[i]) + vd8[g8] * kElem));
-        if (any_hole) {  // what lies in a hole may be NaN, and 0 * NaN is not 0
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (va[i] < 0) rows[i] = u32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t r[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = rows[i][w];
-          u32x4 even, odd;
-          transpose_pair(r, even, odd);
-          f32x4& oe = o[8 * g8 + 2 * w];
-          f32x4& oo = o[8 * g8 + 2 * w + 1];
-          oe = T::mma(lo, even, T::mma(hi, even, oe));
-          oo = T::mma(lo, odd, T::mma(hi, odd, oo));
-        }
+      for (int g = 0; g < G::kEights; ++g) {
+        put_words(w + g * G::kWords, load_as<key_vec>(row + value8_at(g)));
       }
       if constexpr (G::kFours > 0) {
-        u32x2 rows[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rows[i] = R4::wide(R4::load(vbase + (va[i] < 0 ? 0 : va[i]) + vd4 * kElem));
-        if (any_hole) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (va[i] < 0) rows[i] = u32x2{0, 0};
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t r[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = rows[i][w];
-          u32x4 even, odd;
-          transpose_pair(r, even, odd);
-          f32x4& oe = o[8 * G::kEights + 2 * w];
-          f32x4& oo = o[8 * G::kEights + 2 * w + 1];
-          oe = T::mma(lo, even, T::mma(hi, even, oe));
-          oo = T::mma(lo, odd, T::mma(hi, odd, oo));
-        }
+        if constexpr (E4M3) w[G::kEights * G::kWords] = load_as<uint32_t>(row + value4_at());
+        else put_words(w + G::kEights * G::kWords, load_as<u32x2>(row + value4_at()));
       }
     }
+  };
+
+  f32x4 o[G::kDims];
+  float m, sum;
+#pragma unroll
+  for (int e = 0; e < G::kDims; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+  m = -INFINITY;
+  sum = 0.f;
+  if (blocks > 0) {
+    fetch(0);
+    place(0);
+    if (blocks > kSpanBlocks) fetch(1);
+    load_keys(0);
+    load_values(0);
+  }
+  for (int blk = 0; blk < blocks; ++blk) {
+    const int in_span = blk % kSpanBlocks;
+    const uint64_t pair = in_span & 2 ? there[1] : there[0];
+    const uint32_t here = in_span & 1 ? (uint32_t)(pair >> 32) : (uint32_t)pair;
+    const bool more = blk + 1 < blocks;
+    if (in_span == kSpanBlocks - 1 && more) {
+      const int span = blk / kSpanBlocks + 1;
+      place(span);
+      if ((span + 1) * kSpanBlocks < blocks) fetch(span + 1);
+    }
+    // scores of tokens 16 t + 4 grp + r for query `col`
+    f32x4 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < DS; ++st) {
+        u32x4 k = wide8<T, E4M3>(kw[t] + st * G::kWords);
+        if (G::masked(st)) k &= G::mask(st, grp, a.depth);
+        s[t] = T::mma(k, qf[st], s[t]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_keys(blk + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    float x[8], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3] * c;
+    const uint32_t mine = here >> (4 * grp);  // bits 0-3 and 16-19: this lane's tokens
+    if (here != ~0u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) x[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+    if (__ballot(top > m + T::kRaise)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float to = fmaxf(m, top - T::kLift);
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      sum *= f;
+      float fr[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) fr[r] = __shfl(f, 4 * grp + r);
+#pragma unroll
+      for (int e = 0; e < G::kDims; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[e][r] *= fr[r];
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    u32x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p0 = __builtin_amdgcn_exp2f(x[2 * i] - base), p1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - base);
+      sum += p0 + p1;
+      uint32_t h2, l2;
+      T::split(p0, p1, h2, l2);
+      hi[i] = h2;
+      lo[i] = l2;
+    }
+    if (here != ~0u) {  // what lies in a hole may be NaN, and 0 * NaN is not 0
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int w = 0; w < G::kValueWords; ++w)
+          if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) vw[i][w] = 0;
+    }
+    const auto product = [&](const uint32_t(&r)[8], f32x4& oe, f32x4& oo) {
+      u32x4 even, odd;
+      transpose_pair(r, even, odd);
+      oe = T::mma(lo, even, T::mma(hi, even, oe));
+      oo = T::mma(lo, odd, T::mma(hi, odd, oo));
+    };
+#pragma unroll
+    for (int d = 0; d < G::kDims; d += 4) {  // 4 dimensions: two words of 16-bit elements
+      uint32_t r0[8], r1[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (E4M3) {
+          r0[i] = T::template from_e4m3<false>(vw[i][d / 4]);
+          r1[i] = T::template from_e4m3<true>(vw[i][d / 4]);
+        } else {
+          r0[i] = vw[i][d / 2];
+          r1[i] = vw[i][d / 2 + 1];
+        }
+      }
+      product(r0, o[d], o[d + 1]);
+      product(r1, o[d + 2], o[d + 3]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (more) load_values(blk + 1);
   }
 
   // the four waves' parts, joined: thread (query, col) takes a chunk of the sums
@@ -426,33 +501,47 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(Args a) {
 }
 
 // One workgroup per row and query head: its parts, weighted by their maxima.
+// Wave w takes parts w, w + 4, ..; a lane up to 4 dimensions.
 template <class T>
-__global__ __launch_bounds__(64) void join_kernel(Args a) {
+__global__ __launch_bounds__(kThreads) void join_kernel(Args a) {
+  __shared__ float sums[kWaves][256];
+  __shared__ float2 stats[kWaves];
   const int hq = a.heads * a.group;
   const int b = blockIdx.x / hq, h = blockIdx.x - b * hq;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Range all = attended(a, b);
-  const int64_t n = all.end - all.begin, share = split_tokens(n, a.splits);
-  const int parts = n > 0 ? (int)((n + share - 1) / share) : 1;
+  const int share = share_of(a, all), n = all.end - all.begin;
+  const int parts = n > 0 ? (int)((n - 1) / share) + 1 : 1;
   const float2* stat = a.stat + int64_t(blockIdx.x) * a.splits;
   const float* part = a.part + int64_t(blockIdx.x) * a.splits * a.depth;
-  float top = -INFINITY;
-  for (int i = 0; i < parts; ++i) top = fmaxf(top, stat[i].x);
-  float total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < parts; ++i) {
-    const float f = stat[i].y == 0.f ? 0.f : __builtin_amdgcn_exp2f(stat[i].x - top);
-    total += f * stat[i].y;
+  float top = -INFINITY, total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = lane; i < parts; i += 64) top = fmaxf(top, stat[i].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  for (int i = wave; i < parts; i += kWaves) {
+    const float2 z = stat[i];
+    const float f = z.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(z.x - top);
+    total += f * z.y;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int d = threadIdx.x + 64 * e;
+      const int d = lane + 64 * e;
       if (d < a.depth) y[e] += f * part[int64_t(i) * a.depth + d];
     }
   }
-  const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[h / a.group] : 1.f) / total;
-  char* dst = a.out + b * a.o_row + h * a.o_head;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int d = threadIdx.x + 64 * e;
-    if (d < a.depth) ((uint16_t*)dst)[d] = (uint16_t)T::put(total == 0.f ? 0.f : y[e] * g);
+  for (int e = 0; e < 4; ++e) sums[wave][lane + 64 * e] = y[e];
+  if (lane == 0) stats[wave].y = total;
+  __syncthreads();
+  total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) total += stats[w].y;
+  if ((int)threadIdx.x < a.depth) {
+    float all_waves = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) all_waves += sums[w][threadIdx.x];
+    const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[h / a.group] : 1.f) / total;
+    char* dst = a.out + b * a.o_row + h * a.o_head;
+    ((uint16_t*)dst)[threadIdx.x] = (uint16_t)T::put(total == 0.f ? 0.f : all_waves * g);
   }
   if (threadIdx.x == 0 && a.lse) a.lse[blockIdx.x] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
 }
@@ -471,17 +560,22 @@ int check_query(const char* what, const stg_tensor* t, const char* name) {
   return STG_OK;
 }
 
-// Splits of a sequence, from the sizes that the host knows.
-int64_t splits_for(int64_t groups, int64_t longest) {
-  if (groups < 1 || longest < 1) return 1;
-  int64_t n = (kWantGroups + groups - 1) / groups;
-  const int64_t most = (longest + kLeastShare - 1) / kLeastShare;
-  n = n < most ? n : most;
-  return n < 1 ? 1 : n > 1024 ? 1024 : n;
+// Tokens of a split, from the sizes that the host knows, and how many splits
+// the longest row has.
+struct Split {
+  int64_t share, count;
+};
+Split split_for(int64_t groups, int64_t longest) {
+  if (groups < 1 || longest < 1) return Split{kBlock, 1};
+  const int64_t want = (kWantGroups + groups - 1) / groups;
+  int64_t share = (longest + want - 1) / want;
+  share = share < kLeastShare ? kLeastShare : share;
+  share = (share + kBlock * kWaves - 1) / (kBlock * kWaves) * (kBlock * kWaves);
+  return Split{share, (longest + share - 1) / share};
 }
 
 int plan(const char* what, const stg_tensor* q, const stg_tensor* k_cache, const stg_tensor* page_table, int64_t window,
-         int64_t max_len, int64_t* tiles, int64_t* splits, int64_t* bytes) {
+         int64_t max_len, int64_t* tiles, Split* split, int64_t* bytes) {
   if (int rc = check_query(what, q, "q")) return rc;
   if (int rc = check_paged_cache(what, k_cache, k_cache, page_table)) return rc;
   const int64_t heads = k_cache->shape[2], depth = q->shape[2];
@@ -502,10 +596,11 @@ int plan(const char* what, const stg_tensor* q, const stg_tensor* k_cache, const
   int64_t longest = page_table->shape[1] * k_cache->shape[1];  // each below 2^31
   if (max_len && max_len < longest) longest = max_len;
   if (window && window < longest) longest = window;
-  *splits = splits_for(groups, longest);
+  if (longest > INT32_MAX) longest = INT32_MAX;  // a length is an int32
+  *split = split_for(groups, longest);
   *bytes = 0;
-  if (*splits > 1) {
-    const int64_t parts = q->shape[0] * q->shape[1] * *splits;
+  if (split->count > 1) {
+    const int64_t parts = q->shape[0] * q->shape[1] * split->count;
     *bytes = parts * (8 + depth * 4);
   }
   return STG_OK;
@@ -516,12 +611,17 @@ void launch_attention(const Args& a, uint32_t grid, hipStream_t st) {
   const auto go = [&](auto kernel) {
     launch_kernel("paged_attention", kernel, dim3(grid), dim3(kThreads), 0, st, a);
   };
+  const auto pick = [&](auto ds) {
+    constexpr int DS = decltype(ds)::value;
+    if (a.depth == 32 * DS) go(paged_attention_kernel<T, DS, E4M3, false>);
+    else go(paged_attention_kernel<T, DS, E4M3, true>);
+  };
   const int steps = (a.depth + 31) / 32;
-  if (steps <= 2) go(paged_attention_kernel<T, 2, E4M3>);
-  else if (steps == 3) go(paged_attention_kernel<T, 3, E4M3>);
-  else if (steps == 4) go(paged_attention_kernel<T, 4, E4M3>);
-  else if (steps <= 6) go(paged_attention_kernel<T, 6, E4M3>);
-  else go(paged_attention_kernel<T, 8, E4M3>);
+  if (steps <= 2) pick(std::integral_constant<int, 2>{});
+  else if (steps == 3) pick(std::integral_constant<int, 3>{});
+  else if (steps == 4) pick(std::integral_constant<int, 4>{});
+  else if (steps <= 6) pick(std::integral_constant<int, 6>{});
+  else pick(std::integral_constant<int, 8>{});
 }
 
 }  // namespace
@@ -532,8 +632,9 @@ using namespace stg;
 extern "C" int64_t paged_attention_workspace(const stg_tensor* q, const stg_tensor* k_cache,
                                              const stg_tensor* page_table, int64_t window, int64_t max_len) {
   clear_error();
-  int64_t tiles, splits, bytes;
-  if (int rc = plan("paged_attention_workspace", q, k_cache, page_table, window, max_len, &tiles, &splits, &bytes))
+  int64_t tiles, bytes;
+  Split split;
+  if (int rc = plan("paged_attention_workspace", q, k_cache, page_table, window, max_len, &tiles, &split, &bytes))
     return -rc;
   return bytes;
 }
@@ -545,8 +646,9 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
                                void* stream) {
   clear_error();
   const char* what = "paged_attention";
-  int64_t tiles, splits, bytes;
-  if (int rc = plan(what, q, k_cache, page_table, window, max_len, &tiles, &splits, &bytes)) return rc;
+  int64_t tiles, bytes;
+  Split split;
+  if (int rc = plan(what, q, k_cache, page_table, window, max_len, &tiles, &split, &bytes)) return rc;
   if (int rc = check_paged_cache(what, k_cache, v_cache, page_table)) return rc;
   if (int rc = check_query(what, out, "out")) return rc;
   if (out->dtype != q->dtype) return fail(STG_ERR_INVALID, "%s: out has another dtype than q", what);
@@ -596,13 +698,14 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
   a.group = (int32_t)(q->shape[1] / k_cache->shape[2]);
   a.tiles = (int32_t)tiles;
   a.depth = (int32_t)q->shape[2];
-  a.splits = (int32_t)splits;
+  a.splits = (int32_t)split.count;
+  a.share = (int32_t)split.share;
   a.window = window;
-  const int64_t parts = q->shape[0] * q->shape[1] * splits;
+  const int64_t parts = q->shape[0] * q->shape[1] * split.count;
   a.stat = (float2*)workspace;
   a.part = (float*)workspace + 2 * parts;
   int64_t grid;
-  if (__builtin_mul_overflow(int64_t(a.rows) * a.heads * a.tiles, splits, &grid) || grid > (int64_t(1) << 31) - 1 ||
+  if (__builtin_mul_overflow(int64_t(a.rows) * a.heads * a.tiles, split.count, &grid) || grid > (int64_t(1) << 31) - 1 ||
       q->shape[0] * q->shape[1] > (int64_t(1) << 31) - 1)
     return fail(STG_ERR_RANGE, "%s: too many rows and heads", what);
   const hipStream_t st = as_stream(stream);
@@ -615,9 +718,9 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
     else launch_attention<F16, false>(a, (uint32_t)grid, st);
   }
   if (int rc = check_launch(what)) return rc;
-  if (splits == 1) return STG_OK;
+  if (split.count == 1) return STG_OK;
   const dim3 rows((uint32_t)(q->shape[0] * q->shape[1]));
-  if (q->dtype == STG_BF16) launch_kernel("paged_attention/join", join_kernel<BF16>, rows, dim3(64), 0, st, a);
-  else launch_kernel("paged_attention/join", join_kernel<F16>, rows, dim3(64), 0, st, a);
+  if (q->dtype == STG_BF16) launch_kernel("paged_attention/join", join_kernel<BF16>, rows, dim3(kThreads), 0, st, a);
+  else launch_kernel("paged_attention/join", join_kernel<F16>, rows, dim3(kThreads), 0, st, a);
   return check_launch("paged_attention/join");
 }
