@@ -142,11 +142,11 @@ __device__ __forceinline__ void wave_sync() {
 
 __device__ __forceinline__ void put_words(uint32_t* w, u32x4 x) { w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3]; }
 __device__ __forceinline__ void put_words(uint32_t* w, u32x2 x) { w[0] = x[0], w[1] = x[1]; }
+// Non-temporal, at any alignment.
 template <class V>
 __device__ __forceinline__ V load_as(const char* p) {
-  V v;
-  __builtin_memcpy(&v, p, sizeof(V));
-  return v;
+  typedef V any __attribute__((aligned(1)));
+  return __builtin_nontemporal_load((const any*)p);
 }
 
 // DS: depth in steps of 32 (rounded up); E4M3: the caches hold e4m3 codes;
@@ -179,6 +179,23 @@ struct Geometry {
   // steps that can pass the row's end (depth > 32 (DS - 2) for every DS used)
   static __device__ __forceinline__ constexpr bool masked(int step) { return RAGGED && step >= DS - 2; }
 
+  // ---- keys on their way: a wave loads a block's rows in chunks of 16 bytes (8
+  // where codes end anywhere), chunk x of the block by lane x % 64 of load x / 64,
+  // so that a load covers whole rows; through LDS they become operands.
+  static constexpr int kChunk = E4M3 && RAGGED ? 8 : 16;  // bytes
+  static constexpr int kChunks = 32 * DS * (E4M3 ? 1 : 2) / kChunk;  // of a row
+  static constexpr int kLoads = kBlock * kChunks / 64;
+  static constexpr int kPeriod = kChunks % 3 ? 1 : 3;  // loads after which a lane has the same chunk, kRows rows on
+  static constexpr int kRows = 64 * kPeriod / kChunks;
+  // bytes of a row in LDS: an odd number of chunks, so that 16 rows' chunks lie
+  // in 16 different places of the banks
+  static constexpr int kPitch = (kChunks | 1) * kChunk;
+  static constexpr int kTile = kBlock * kPitch;
+  static __device__ __forceinline__ int chunk_from(int chunk, int depth) {
+    const int d = chunk * (kChunk / (E4M3 ? 1 : 2));
+    return RAGGED && d > depth - 8 ? depth - 8 : d;
+  }
+
   // ---- values: a lane's share of a row, in dimensions: chunks of 8 over 128
   // dimensions, one chunk of 4 for a rest of 64
   static constexpr int kDims = DS <= 2 ? 4 : DS <= 4 ? 8 : DS <= 6 ? 12 : 16;
@@ -189,13 +206,13 @@ struct Geometry {
   static constexpr bool kExact = !RAGGED && 16 * kDims == 32 * DS;
 };
 
-template <class T, bool E4M3>
-__device__ __forceinline__ u32x4 wide8(const uint32_t* w) {
+template <class T, bool E4M3, class V>
+__device__ __forceinline__ u32x4 wide8(V w) {
   if constexpr (E4M3)
     return u32x4{T::template from_e4m3<false>(w[0]), T::template from_e4m3<true>(w[0]),
                  T::template from_e4m3<false>(w[1]), T::template from_e4m3<true>(w[1])};
   else
-    return u32x4{w[0], w[1], w[2], w[3]};
+    return w;
 }
 
 // Elements 2w and 2w+1 of eight rows -> the two operands that hold one
@@ -212,10 +229,12 @@ template <class T, int DS, bool E4M3, bool RAGGED>
 __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged_attention_kernel(Args a) {
   using G = Geometry<T, DS, E4M3, RAGGED>;
   constexpr int kElem = E4M3 ? 1 : 2;
-  // token addresses during the loop (two spans a wave), the waves' sums after it
+  // token addresses (two spans a wave) and a block's keys during the loop, the
+  // waves' sums after it
   __shared__ union {
     struct {
       int64_t k[kWaves][2][kSpan], v[kWaves][2][kSpan];
+      __attribute__((aligned(16))) char keys[kWaves][G::kTile];
     } at;
     float sums[kWaves][kQueries][128];
   } lds;
@@ -256,12 +275,18 @@ __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged
     }
   }
   const float c = a.scale_log2 * (a.k_scale ? a.k_scale[h] : 1.f);
-  const char* kbase = a.k + h * a.k_head + (RAGGED ? 0 : G::dim(0, grp) * kElem);
+  const char* kbase = a.k + h * a.k_head;
+  int key_row[G::kPeriod], key_from[G::kPeriod], key_to[G::kPeriod];
+#pragma unroll
+  for (int i = 0; i < G::kPeriod; ++i) {
+    const int x = 64 * i + lane;
+    key_row[i] = x / G::kChunks;
+    const int chunk = x - key_row[i] * G::kChunks;
+    key_from[i] = G::chunk_from(chunk, a.depth) * kElem;
+    key_to[i] = key_row[i] * G::kPitch + chunk * G::kChunk;
+  }
   const char* vbase = a.v + h * a.v_head + (G::kExact ? (G::kEights ? 8 : 4) * col * kElem : 0);
   // where this lane's chunks begin, from those bases
-  const auto key_at = [&](int s) {
-    return (RAGGED ? G::from(s, grp, a.depth) : G::dim(s, grp) - G::dim(0, grp)) * kElem;
-  };
   const auto value8_at = [&](int i) {
     const int d = 128 * i + 8 * col;
     return (G::kExact ? 128 * i : d < a.depth - 8 ? d : a.depth - 8) * kElem;
@@ -298,25 +323,32 @@ __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged
     wave_sync();
   };
 
-  using key_vec = std::conditional_t<E4M3, u32x2, u32x4>;  // 8 elements
-  uint32_t kw[2][DS * G::kWords];   // keys of tokens col and 16 + col
+  using chunk_vec = std::conditional_t<G::kChunk == 8, u32x2, u32x4>;
+  using value_vec = std::conditional_t<E4M3, u32x2, u32x4>;  // 8 elements
+  chunk_vec kv[G::kLoads];          // the block's keys on their way to LDS
   uint32_t vw[8][G::kValueWords];   // values of tokens 4 grp + i, 12 + 4 grp + i (i >= 4)
   const auto load_keys = [&](int blk) {
     const int64_t* k = &lds.at.k[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const char* row = kbase + k[16 * t + col];
-#pragma unroll
-      for (int s = 0; s < DS; ++s) {
-        uint32_t* w = kw[t] + s * G::kWords;
-        if (G::kPairs && (s | 1) < DS) {
-          if (s & 1) continue;  // came with the step before
-          put_words(w, load_as<u32x4>(row + key_at(s)));
-        } else {
-          put_words(w, load_as<key_vec>(row + key_at(s)));
-        }
-      }
+    for (int i = 0; i < G::kLoads; ++i) {
+      const int j = i % G::kPeriod;
+      kv[i] = load_as<chunk_vec>(kbase + k[key_row[j] + i / G::kPeriod * G::kRows] + key_from[j]);
     }
+  };
+  char* const keys = lds.at.keys[wave];
+  const auto store_keys = [&]() {
+    wave_sync();  // the block before is read
+#pragma unroll
+    for (int i = 0; i < G::kLoads; ++i)
+      *(chunk_vec*)(keys + key_to[i % G::kPeriod] + i / G::kPeriod * G::kRows * G::kPitch) = kv[i];
+    wave_sync();
+  };
+  // 8 elements of token 16 t + col
+  const auto key_words = [&](int t, int st) {
+    const char* row = keys + (16 * t + col) * G::kPitch;
+    if constexpr (!E4M3) return *(const u32x4*)(row + (4 * st + grp) * 16);
+    else if constexpr (RAGGED) return *(const u32x2*)(row + (4 * st + grp) * 8);
+    else return *(const u32x2*)(row + G::dim(st, grp));
   };
   const auto load_values = [&](int blk) {
     const int64_t* v = &lds.at.v[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
@@ -326,7 +358,7 @@ __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged
       uint32_t* w = vw[i];
 #pragma unroll
       for (int g = 0; g < G::kEights; ++g) {
-        put_words(w + g * G::kWords, load_as<key_vec>(row + value8_at(g)));
+        put_words(w + g * G::kWords, load_as<value_vec>(row + value8_at(g)));
       }
       if constexpr (G::kFours > 0) {
         if constexpr (E4M3) w[G::kEights * G::kWords] = load_as<uint32_t>(row + value4_at());
@@ -358,6 +390,7 @@ __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged
       place(span);
       if ((span + 1) * kSpanBlocks < blocks) fetch(span + 1);
     }
+    store_keys();
     // scores of tokens 16 t + 4 grp + r for query `col`
     f32x4 s[2];
 #pragma unroll
@@ -365,7 +398,7 @@ __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged
       s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
-        u32x4 k = wide8<T, E4M3>(kw[t] + st * G::kWords);
+        u32x4 k = wide8<T, E4M3>(key_words(t, st));
         if (G::masked(st)) k &= G::mask(st, grp, a.depth);
         s[t] = T::mma(k, qf[st], s[t]);
       }
