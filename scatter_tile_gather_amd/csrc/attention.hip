@@ -2,26 +2,39 @@
 //
 // Every cached key and value is read once, so HBM bounds the call; the design
 // keeps all else off that path.
-//  - A workgroup takes one cache head of one sequence over a part of its
-//    tokens, for up to 16 of the query heads that share it.  Its four waves
-//    walk over blocks of 32 tokens.
+//  - A workgroup takes tokens of one cache head, for up to 16 of the query heads
+//    that share it.  Rows of up to 1024 tokens go to one workgroup each.  For
+//    longer ones the tokens of all rows, end to end, are cut into as many equal
+//    chunks as the chip holds workgroups, so that all end together however
+//    ragged the rows are, and a second kernel joins the rows that were cut.
+//    64 rows of 1 .. 8192 tokens, 8 heads of 128, bf16: 183 us (6.0 TB/s of keys
+//    and values); cut row by row into parts of 1024 tokens: 201 us.
+//  - Its four waves each take a quarter of a row's tokens and walk over blocks
+//    of 32.  A block's keys and values are loaded into registers while the
+//    block before is computed; its addresses come from LDS, a span of 128
+//    tokens ahead.  There is no barrier in the loop.
 //  - Scores are computed transposed, S^T = K Q^T (v_mfma 16x16x32): a lane then
 //    holds, for query l % 16, the scores of 8 of the 32 tokens -- just the
 //    elements that the second product wants as its left operand P, so
 //    probabilities never cross lanes.  The 8 tokens that lane group g = l / 16
 //    holds are 4g .. 4g+3 and 16+4g .. 16+4g+3; the sum over tokens may take
 //    them in any order as long as V is fed in the same one.
-//  - K rows go from memory to the matrix unit as they are (a lane's 16 bytes
-//    are its operand).  V is wanted with 8 tokens of one dimension in a lane
-//    but lies with 8 dimensions of one token in 16 bytes: a lane loads 8 x 8
-//    elements and transposes them with byte permutes in its own registers.
-//    Nothing of K or V passes through LDS, and there is no barrier in the loop.
+//  - Loads cover whole rows, 256 contiguous bytes in 16 lanes: read as matrix
+//    operands straight away, K would come in pieces of 64 bytes of 16 rows, and
+//    that costs a seventh (231 us instead of 201 above).  K's rows become operands
+//    through LDS.  V is wanted with 8 tokens of one dimension in a lane but lies
+//    with 8 dimensions of one token in 16 bytes: a lane loads 8 x 8 elements and
+//    transposes them with byte permutes in its own registers.
+//  - Where rows are whole cache lines, loads are non-temporal (224 us without).
+//    Where they are not, neighbouring heads share lines: then the heads of a
+//    token run on one XCD, whose L2 keeps the line for the next (depth 100,
+//    64 rows of up to 4096 tokens: 109 us; non-temporal and spread over XCDs 138).
 //  - One pass, with a running maximum that is raised only when a score exceeds
-//    it by 2^8: until then p = 2^(s - m) <= 2^8 fits, and the usual iteration
-//    needs no exchange between lanes and no rescaling.
-//  - P is fed to the matrix unit as two 16-bit terms, the rounded value and the
-//    rounded rest, so that its rounding (2^-9 of a term in bf16) does not add
-//    to the output's; the product is far from being the bound.
+//    it by a margin (kRaise): the usual iteration needs no exchange between
+//    lanes and no rescaling.
+//  - P is fed to the matrix unit as two 16-bit terms, its leading bits and the
+//    rest, so that its rounding (2^-9 of a term in bf16) does not add to the
+//    output's; the product is far from being the bound.
 #include <type_traits>
 
 #include "stg_internal.h"
@@ -52,11 +65,15 @@ struct Args {
   const float* k_scale;
   const float* v_scale;
   float* lse;
-  float* part;   // (rows, q_heads, splits, depth): sums relative to the part's maximum
-  float2* stat;  // (rows, q_heads, splits): maximum (log2) and sum
+  // split rows (chunks > 0): (q_heads, chunks, 2), the second place for the row
+  // that begins in the chunk and goes on past it, the first for one from before
+  float* part;   // .. of depth: sums relative to the part's maximum
+  float2* stat;  // maximum (log2) and sum
+  int2* plan;    // per chunk: the row that begins in it and goes on, and over how many chunks
   float scale_log2;
   int32_t rows, width, pages, slots;
-  int32_t heads, group, tiles, depth, splits, share;  // share: tokens of a split
+  int32_t heads, group, tiles, depth;
+  int32_t chunks;  // 0: a workgroup takes a row; else the rows' tokens, end to end, are cut into this many
   int64_t window;
 };
 
@@ -124,12 +141,17 @@ __device__ __forceinline__ Range attended(const Args& a, int32_t b) {
   return Range{(int32_t)begin, (int32_t)len};
 }
 
-// Tokens of a split of this row: the host's, or more where the row is longer
-// than the host was told.
-__device__ __forceinline__ int share_of(const Args& a, const Range& all) {
-  const int n = all.end - all.begin;
-  if (n <= int64_t(a.share) * a.splits) return a.share;
-  return (n - 1) / a.splits + 1;
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
+}
+
+// Tokens of a chunk.
+constexpr int64_t kLeastShare = 256;
+__device__ __forceinline__ int64_t share_of(int64_t total, int32_t chunks) {
+  const int64_t n = ((total + chunks - 1) / chunks + kBlock - 1) / kBlock * kBlock;
+  return n < kLeastShare ? kLeastShare : n;
 }
 
 // Orders a wave's LDS accesses against each other: the LDS unit runs one
@@ -142,17 +164,21 @@ __device__ __forceinline__ void wave_sync() {
 
 __device__ __forceinline__ void put_words(uint32_t* w, u32x4 x) { w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3]; }
 __device__ __forceinline__ void put_words(uint32_t* w, u32x2 x) { w[0] = x[0], w[1] = x[1]; }
-// Non-temporal, at any alignment.
-template <class V>
+// At any alignment; NT: non-temporal.
+template <class V, bool NT>
 __device__ __forceinline__ V load_as(const char* p) {
   typedef V any __attribute__((aligned(1)));
-  return __builtin_nontemporal_load((const any*)p);
+  if constexpr (NT) return __builtin_nontemporal_load((const any*)p);
+  else return *(const any*)p;
 }
 
 // DS: depth in steps of 32 (rounded up); E4M3: the caches hold e4m3 codes;
 // RAGGED: depth is not 32 DS.
 template <class T, int DS, bool E4M3, bool RAGGED>
 struct Geometry {
+  // A row is a number of whole cache lines, as far as its size goes.
+  static constexpr bool kLines = !RAGGED && 32 * DS * (E4M3 ? 1 : 2) % 128 == 0;
+
   // ---- queries and keys: a lane of group grp holds 8 dimensions of each step
   // of 32.  Which ones is free as long as both sides agree: 8 codes are only 8
   // bytes, so pairs of steps take 16 codes in a row with one load.
@@ -225,8 +251,11 @@ __device__ __forceinline__ void transpose_pair(const uint32_t (&r)[8], u32x4& ev
   }
 }
 
+// Waves of a SIMD that the registers are shared out to.
+constexpr int waves_for(int ds, bool e4m3) { return ds <= 2 ? 4 : ds <= 4 ? 3 : ds <= 6 || e4m3 ? 2 : 1; }
+
 template <class T, int DS, bool E4M3, bool RAGGED>
-__global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged_attention_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention_kernel(Args a) {
   using G = Geometry<T, DS, E4M3, RAGGED>;
   constexpr int kElem = E4M3 ? 1 : 2;
   // token addresses (two spans a wave) and a block's keys during the loop, the
@@ -240,334 +269,430 @@ __global__ __launch_bounds__(kThreads, DS <= 2 ? 4 : DS <= 4 ? 3 : 2) void paged
   } lds;
   __shared__ float2 stats[kWaves][kQueries];
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, grp = lane >> 4;
-  uint32_t id = blockIdx.x;
+  uint32_t id = G::kLines ? blockIdx.x : xcd_remap(blockIdx.x, gridDim.x);
   const int h = id % a.heads;
   id /= a.heads;
   const int tile = id % a.tiles;
   id /= a.tiles;
-  const int split = id % a.splits;
-  const int b = id / a.splits;
+  // A workgroup's tokens: row id, or chunk id of all rows' tokens end to end,
+  // [t0, t0 + share), and the rows that begin in it, those without a token among
+  // them.  b and before: its first row, and how many tokens come before that.
+  int b = id;
+  int64_t before = 0, t0 = 0, share = 0;
+  bool last = false;
+  if (a.chunks) {
+    __shared__ int64_t sums[kWaves], found_before;
+    __shared__ int32_t found;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = (a.rows + kThreads - 1) / kThreads;
+    const int r0 = threadIdx.x * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) {
+      const Range t = attended(a, r);
+      mine += t.end - t.begin;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t x = __shfl_up(upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 63) sums[wave] = upto;
+    if (threadIdx.x == 0) found = a.rows;
+    __syncthreads();
+    int64_t total = 0;
+    before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? sums[w] : 0;
+      total += sums[w];
+    }
+    total = uniform(total);
+    share = share_of(total, a.chunks);
+    t0 = id * share;
+    last = t0 + share >= total;
+    if (id > 0 && t0 >= total) {
+      if (h == 0 && tile == 0 && threadIdx.x == 0) a.plan[id] = make_int2(-1, 0);
+      return;
+    }
+    int first = a.rows;
+    for (int r = r0; r < r1; ++r) {
+      const Range t = attended(a, r);
+      if (before >= t0 || before + (t.end - t.begin) > t0) {
+        first = r;
+        break;
+      }
+      before += t.end - t.begin;
+    }
+    if (first < a.rows) atomicMin(&found, first);
+    __syncthreads();
+    if (first == found) found_before = before;
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(found);
+    before = uniform(found_before);
+  }
+  int2 goes_on = make_int2(-1, 0);
 
-  const Range all = attended(a, b);
-  const int share = share_of(a, all);
-  const int64_t part_begin = all.begin + int64_t(split) * share;
-  if (part_begin >= all.end && split > 0) return;  // the join knows which parts exist
-  const int part_tokens = all.end - part_begin < share ? (int)(all.end - part_begin) : share;
-  // a wave takes a run of tokens, whole blocks but for the last
-  const int run = (part_tokens + kWaves * kBlock - 1) / (kWaves * kBlock) * kBlock;
-  const int left = part_tokens - wave * run;
-  const int n = left < 0 ? 0 : left < run ? left : run;
-  const uint32_t begin = (uint32_t)part_begin + wave * run;
-  const int blocks = (n + kBlock - 1) / kBlock;
-
-  // queries: operand column `col`
   const int head0 = h * a.group + tile * kQueries;
   const int queries = a.group - tile * kQueries < kQueries ? a.group - tile * kQueries : kQueries;
-  u32x4 qf[DS];
-  {
-    const char* q = a.q + b * a.q_row + (head0 + (col < queries ? col : 0)) * a.q_head;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) {
-      const u32x4 x = ld16(q + 2 * G::from(s, grp, a.depth));
-      qf[s] = col < queries ? x & G::mask(s, grp, a.depth) : u32x4{0, 0, 0, 0};
-    }
-  }
   const float c = a.scale_log2 * (a.k_scale ? a.k_scale[h] : 1.f);
-  const char* kbase = a.k + h * a.k_head;
-  int key_row[G::kPeriod], key_from[G::kPeriod], key_to[G::kPeriod];
-#pragma unroll
-  for (int i = 0; i < G::kPeriod; ++i) {
-    const int x = 64 * i + lane;
-    key_row[i] = x / G::kChunks;
-    const int chunk = x - key_row[i] * G::kChunks;
-    key_from[i] = G::chunk_from(chunk, a.depth) * kElem;
-    key_to[i] = key_row[i] * G::kPitch + chunk * G::kChunk;
-  }
-  const char* vbase = a.v + h * a.v_head + (G::kExact ? (G::kEights ? 8 : 4) * col * kElem : 0);
-  // where this lane's chunks begin, from those bases
-  const auto value8_at = [&](int i) {
-    const int d = 128 * i + 8 * col;
-    return (G::kExact ? 128 * i : d < a.depth - 8 ? d : a.depth - 8) * kElem;
-  };
-  const auto value4_at = [&]() {
-    const int d = 128 * G::kEights + 4 * col;
-    return (G::kExact ? (G::kEights ? d - 8 * col : 0) : d < a.depth - 4 ? d : a.depth - 4) * kElem;
-  };
-
-  // A span's addresses: its pages are loaded a span ahead, its offsets go to
-  // LDS when the loop reaches it.  A token without a page has offset 0, which
-  // may be read, and a zero in `there`.
-  int32_t page[2];
-  const auto fetch = [&](int span) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int i = span * kSpan + 64 * t + lane;
-      page[t] = i < n ? a.table[b * a.table_stride + (begin + i) / (uint32_t)a.slots] : -1;
+  for (;;) {
+    // What a lane derives from its number is derived anew for each row: kept
+    // over the loop it would not fit into the registers.
+    uint32_t thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
+    const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
+    const int col = lane & 15, grp = lane >> 4;
+    Range all = attended(a, b);
+    all.begin = __builtin_amdgcn_readfirstlane(all.begin);
+    all.end = __builtin_amdgcn_readfirstlane(all.end);
+    const int tokens = all.end - all.begin;
+    int from = 0, to = tokens;  // of the row's attended tokens
+    if (a.chunks) {
+      from = before < t0 ? (int)(t0 - before) : 0;
+      to = before + tokens > t0 + share ? (int)(t0 + share - before) : tokens;
     }
-  };
-  uint64_t there[2];
-  const auto place = [&](int span) {
-    int64_t* k = lds.at.k[wave][span & 1];
-    int64_t* v = lds.at.v[wave][span & 1];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t j = begin + span * kSpan + 64 * t + lane;
-      const int64_t slot = j % (uint32_t)a.slots;
-      const bool ok = (uint32_t)page[t] < (uint32_t)a.pages;
-      k[64 * t + lane] = ok ? page[t] * a.k_page + slot * a.k_slot : 0;
-      v[64 * t + lane] = ok ? page[t] * a.v_page + slot * a.v_slot : 0;
-      there[t] = __ballot(ok);
-    }
-    wave_sync();
-  };
-
-  using chunk_vec = std::conditional_t<G::kChunk == 8, u32x2, u32x4>;
-  using value_vec = std::conditional_t<E4M3, u32x2, u32x4>;  // 8 elements
-  chunk_vec kv[G::kLoads];          // the block's keys on their way to LDS
-  uint32_t vw[8][G::kValueWords];   // values of tokens 4 grp + i, 12 + 4 grp + i (i >= 4)
-  const auto load_keys = [&](int blk) {
-    const int64_t* k = &lds.at.k[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
-#pragma unroll
-    for (int i = 0; i < G::kLoads; ++i) {
-      const int j = i % G::kPeriod;
-      kv[i] = load_as<chunk_vec>(kbase + k[key_row[j] + i / G::kPeriod * G::kRows] + key_from[j]);
-    }
-  };
-  char* const keys = lds.at.keys[wave];
-  const auto store_keys = [&]() {
-    wave_sync();  // the block before is read
-#pragma unroll
-    for (int i = 0; i < G::kLoads; ++i)
-      *(chunk_vec*)(keys + key_to[i % G::kPeriod] + i / G::kPeriod * G::kRows * G::kPitch) = kv[i];
-    wave_sync();
-  };
-  // 8 elements of token 16 t + col
-  const auto key_words = [&](int t, int st) {
-    const char* row = keys + (16 * t + col) * G::kPitch;
-    if constexpr (!E4M3) return *(const u32x4*)(row + (4 * st + grp) * 16);
-    else if constexpr (RAGGED) return *(const u32x2*)(row + (4 * st + grp) * 8);
-    else return *(const u32x2*)(row + G::dim(st, grp));
-  };
-  const auto load_values = [&](int blk) {
-    const int64_t* v = &lds.at.v[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const char* row = vbase + v[16 * (i >> 2) + 4 * grp + (i & 3)];
-      uint32_t* w = vw[i];
-#pragma unroll
-      for (int g = 0; g < G::kEights; ++g) {
-        put_words(w + g * G::kWords, load_as<value_vec>(row + value8_at(g)));
+    const int jq = thread >> 4;
+    const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
+    if (tokens == 0) {
+      if (jq < queries) {
+        uint16_t* dst = (uint16_t*)(a.out + b * a.o_row + (head0 + jq) * a.o_head);
+        for (int d = col; d < a.depth; d += 16) dst[d] = 0;
+        if (col == 0 && a.lse) a.lse[head] = -INFINITY;
       }
-      if constexpr (G::kFours > 0) {
-        if constexpr (E4M3) w[G::kEights * G::kWords] = load_as<uint32_t>(row + value4_at());
-        else put_words(w + G::kEights * G::kWords, load_as<u32x2>(row + value4_at()));
-      }
-    }
-  };
+    } else {
+      // a wave takes a run of tokens, whole blocks but for the last
+      const int run = (to - from + kWaves * kBlock - 1) / (kWaves * kBlock) * kBlock;
+      const int left = to - from - wave * run;
+      const int n = left < 0 ? 0 : left < run ? left : run;
+      const uint32_t begin = (uint32_t)(all.begin + from) + wave * run;
+      const int blocks = (n + kBlock - 1) / kBlock;
 
-  f32x4 o[G::kDims];
-  float m, sum;
+      // queries: operand column `col`
+      u32x4 qf[DS];
+      {
+        const char* q = a.q + b * a.q_row + (head0 + (col < queries ? col : 0)) * a.q_head;
 #pragma unroll
-  for (int e = 0; e < G::kDims; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-  m = -INFINITY;
-  sum = 0.f;
-  if (blocks > 0) {
-    fetch(0);
-    place(0);
-    if (blocks > kSpanBlocks) fetch(1);
-    load_keys(0);
-    load_values(0);
-  }
-  for (int blk = 0; blk < blocks; ++blk) {
-    const int in_span = blk % kSpanBlocks;
-    const uint64_t pair = in_span & 2 ? there[1] : there[0];
-    const uint32_t here = in_span & 1 ? (uint32_t)(pair >> 32) : (uint32_t)pair;
-    const bool more = blk + 1 < blocks;
-    if (in_span == kSpanBlocks - 1 && more) {
-      const int span = blk / kSpanBlocks + 1;
-      place(span);
-      if ((span + 1) * kSpanBlocks < blocks) fetch(span + 1);
-    }
-    store_keys();
-    // scores of tokens 16 t + 4 grp + r for query `col`
-    f32x4 s[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int st = 0; st < DS; ++st) {
-        u32x4 k = wide8<T, E4M3>(key_words(t, st));
-        if (G::masked(st)) k &= G::mask(st, grp, a.depth);
-        s[t] = T::mma(k, qf[st], s[t]);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (more) load_keys(blk + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    float x[8], top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3] * c;
-    const uint32_t mine = here >> (4 * grp);  // bits 0-3 and 16-19: this lane's tokens
-    if (here != ~0u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) x[i] = -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
-    if (__ballot(top > m + T::kRaise)) {
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float to = fmaxf(m, top - T::kLift);
-      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      sum *= f;
-      float fr[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) fr[r] = __shfl(f, 4 * grp + r);
-#pragma unroll
-      for (int e = 0; e < G::kDims; ++e)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[e][r] *= fr[r];
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    u32x4 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p0 = __builtin_amdgcn_exp2f(x[2 * i] - base), p1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - base);
-      sum += p0 + p1;
-      uint32_t h2, l2;
-      T::split(p0, p1, h2, l2);
-      hi[i] = h2;
-      lo[i] = l2;
-    }
-    if (here != ~0u) {  // what lies in a hole may be NaN, and 0 * NaN is not 0
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int w = 0; w < G::kValueWords; ++w)
-          if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) vw[i][w] = 0;
-    }
-    const auto product = [&](const uint32_t(&r)[8], f32x4& oe, f32x4& oo) {
-      u32x4 even, odd;
-      transpose_pair(r, even, odd);
-      oe = T::mma(lo, even, T::mma(hi, even, oe));
-      oo = T::mma(lo, odd, T::mma(hi, odd, oo));
-    };
-#pragma unroll
-    for (int d = 0; d < G::kDims; d += 4) {  // 4 dimensions: two words of 16-bit elements
-      uint32_t r0[8], r1[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (E4M3) {
-          r0[i] = T::template from_e4m3<false>(vw[i][d / 4]);
-          r1[i] = T::template from_e4m3<true>(vw[i][d / 4]);
-        } else {
-          r0[i] = vw[i][d / 2];
-          r1[i] = vw[i][d / 2 + 1];
+        for (int s = 0; s < DS; ++s) {
+          const u32x4 x = ld16(q + 2 * G::from(s, grp, a.depth));
+          qf[s] = col < queries ? x & G::mask(s, grp, a.depth) : u32x4{0, 0, 0, 0};
         }
       }
-      product(r0, o[d], o[d + 1]);
-      product(r1, o[d + 2], o[d + 3]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (more) load_values(blk + 1);
-  }
 
-  // the four waves' parts, joined: thread (query, col) takes a chunk of the sums
-  sum += __shfl_xor(sum, 16);
-  sum += __shfl_xor(sum, 32);
-  if (grp == 0) stats[wave][col] = make_float2(m, sum);
-  const int jq = threadIdx.x >> 4;
-  const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
-  float f[kWaves], top = -INFINITY, total = 0.f;
+      const char* kbase = a.k + h * a.k_head;
+      int key_row[G::kPeriod], key_from[G::kPeriod], key_to[G::kPeriod];
 #pragma unroll
-  for (int piece = 0; piece < G::kEights + G::kFours; ++piece) {
-    const int n = piece < G::kEights ? 8 : 4;
-    __syncthreads();  // the loop's addresses, or the last piece, are read
+      for (int i = 0; i < G::kPeriod; ++i) {
+        const int x = 64 * i + lane;
+        key_row[i] = x / G::kChunks;
+        const int chunk = x - key_row[i] * G::kChunks;
+        key_from[i] = G::chunk_from(chunk, a.depth) * kElem;
+        key_to[i] = key_row[i] * G::kPitch + chunk * G::kChunk;
+      }
+      const char* vbase = a.v + h * a.v_head + (G::kExact ? (G::kEights ? 8 : 4) * col * kElem : 0);
+      // where this lane's chunks begin, from those bases
+      const auto value8_at = [&](int i) {
+        const int d = 128 * i + 8 * col;
+        return (G::kExact ? 128 * i : d < a.depth - 8 ? d : a.depth - 8) * kElem;
+      };
+      const auto value4_at = [&]() {
+        const int d = 128 * G::kEights + 4 * col;
+        return (G::kExact ? (G::kEights ? d - 8 * col : 0) : d < a.depth - 4 ? d : a.depth - 4) * kElem;
+      };
+
+      // A span's addresses: its pages are loaded a span ahead, its offsets go to
+      // LDS when the loop reaches it.  A token without a page has offset 0, which
+      // may be read, and a zero in `there`.
+      int32_t page[2];
+      const auto fetch = [&](int span) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n)
+        for (int t = 0; t < 2; ++t) {
+          const int i = span * kSpan + 64 * t + lane;
+          page[t] = i < n ? a.table[b * a.table_stride + (begin + i) / (uint32_t)a.slots] : -1;
+        }
+      };
+      uint64_t there[2];
+      const auto place = [&](int span) {
+        int64_t* k = lds.at.k[wave][span & 1];
+        int64_t* v = lds.at.v[wave][span & 1];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) lds.sums[wave][4 * grp + r][col * n + e] = o[8 * piece + e < G::kDims ? 8 * piece + e : 0][r];
-    __syncthreads();
-    if (piece == 0) {
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t j = begin + span * kSpan + 64 * t + lane;
+          const int64_t slot = j % (uint32_t)a.slots;
+          const bool ok = (uint32_t)page[t] < (uint32_t)a.pages;
+          k[64 * t + lane] = ok ? page[t] * a.k_page + slot * a.k_slot : 0;
+          v[64 * t + lane] = ok ? page[t] * a.v_page + slot * a.v_slot : 0;
+          there[t] = __ballot(ok);
+        }
+        wave_sync();
+      };
+
+      using chunk_vec = std::conditional_t<G::kChunk == 8, u32x2, u32x4>;
+      using value_vec = std::conditional_t<E4M3, u32x2, u32x4>;  // 8 elements
+      chunk_vec kv[G::kLoads];          // the block's keys on their way to LDS
+      uint32_t vw[8][G::kValueWords];   // values of tokens 4 grp + i, 12 + 4 grp + i (i >= 4)
+      const auto load_keys = [&](int blk) {
+        const int64_t* k = &lds.at.k[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[w][jq].x);
+        for (int i = 0; i < G::kLoads; ++i) {
+          const int j = i % G::kPeriod;
+          kv[i] = load_as<chunk_vec, G::kLines>(kbase + k[key_row[j] + i / G::kPeriod * G::kRows] + key_from[j]);
+        }
+      };
+      char* const keys = lds.at.keys[wave];
+      const auto store_keys = [&]() {
+        wave_sync();  // the block before is read
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        f[w] = stats[w][jq].y == 0.f ? 0.f : __builtin_amdgcn_exp2f(stats[w][jq].x - top);
-        total += f[w] * stats[w][jq].y;
+        for (int i = 0; i < G::kLoads; ++i)
+          *(chunk_vec*)(keys + key_to[i % G::kPeriod] + i / G::kPeriod * G::kRows * G::kPitch) = kv[i];
+        wave_sync();
+      };
+      // 8 elements of token 16 t + col
+      const auto key_words = [&](int t, int st) {
+        const char* row = keys + (16 * t + col) * G::kPitch;
+        if constexpr (!E4M3) return *(const u32x4*)(row + (4 * st + grp) * 16);
+        else if constexpr (RAGGED) return *(const u32x2*)(row + (4 * st + grp) * 8);
+        else return *(const u32x2*)(row + G::dim(st, grp));
+      };
+      const auto load_values = [&](int blk) {
+        const int64_t* v = &lds.at.v[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const char* row = vbase + v[16 * (i >> 2) + 4 * grp + (i & 3)];
+          uint32_t* w = vw[i];
+#pragma unroll
+          for (int g = 0; g < G::kEights; ++g) {
+            put_words(w + g * G::kWords, load_as<value_vec, G::kLines>(row + value8_at(g)));
+          }
+          if constexpr (G::kFours > 0) {
+            if constexpr (E4M3) w[G::kEights * G::kWords] = load_as<uint32_t, G::kLines>(row + value4_at());
+            else put_words(w + G::kEights * G::kWords, load_as<u32x2, G::kLines>(row + value4_at()));
+          }
+        }
+      };
+
+      f32x4 o[G::kDims];
+      float m, sum;
+#pragma unroll
+      for (int e = 0; e < G::kDims; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+      m = -INFINITY;
+      sum = 0.f;
+      // (set where no block follows, so that nothing lives on from the row before)
+#pragma unroll
+      for (int i = 0; i < G::kLoads; ++i) kv[i] = chunk_vec{};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int w = 0; w < G::kValueWords; ++w) vw[i][w] = 0;
+      page[0] = page[1] = -1;
+      there[0] = there[1] = 0;
+      if (blocks > 0) {
+        fetch(0);
+        place(0);
+        if (blocks > kSpanBlocks) fetch(1);
+        load_keys(0);
+        load_values(0);
+      }
+      for (int blk = 0; blk < blocks; ++blk) {
+        const int in_span = blk % kSpanBlocks;
+        const uint64_t pair = in_span & 2 ? there[1] : there[0];
+        const uint32_t here = in_span & 1 ? (uint32_t)(pair >> 32) : (uint32_t)pair;
+        const bool more = blk + 1 < blocks;
+        if (in_span == kSpanBlocks - 1 && more) {
+          const int span = blk / kSpanBlocks + 1;
+          place(span);
+          if ((span + 1) * kSpanBlocks < blocks) fetch(span + 1);
+        }
+        store_keys();
+        // scores of tokens 16 t + 4 grp + r for query `col`
+        f32x4 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int st = 0; st < DS; ++st) {
+            u32x4 k = wide8<T, E4M3>(key_words(t, st));
+            if (G::masked(st)) k &= G::mask(st, grp, a.depth);
+            s[t] = T::mma(k, qf[st], s[t]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) load_keys(blk + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        float x[8], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s[i >> 2][i & 3] * c;
+        const uint32_t mine = here >> (4 * grp);  // bits 0-3 and 16-19: this lane's tokens
+        if (here != ~0u) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) x[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+        if (__ballot(top > m + T::kRaise)) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float to = fmaxf(m, top - T::kLift);
+          const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - to);
+          m = to;
+          sum *= f;
+          float fr[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) fr[r] = __shfl(f, 4 * grp + r);
+#pragma unroll
+          for (int e = 0; e < G::kDims; ++e)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[e][r] *= fr[r];
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        u32x4 hi, lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p0 = __builtin_amdgcn_exp2f(x[2 * i] - base), p1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - base);
+          sum += p0 + p1;
+          uint32_t h2, l2;
+          T::split(p0, p1, h2, l2);
+          hi[i] = h2;
+          lo[i] = l2;
+        }
+        if (here != ~0u) {  // what lies in a hole may be NaN, and 0 * NaN is not 0
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int w = 0; w < G::kValueWords; ++w)
+              if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) vw[i][w] = 0;
+        }
+        const auto product = [&](const uint32_t(&r)[8], f32x4& oe, f32x4& oo) {
+          u32x4 even, odd;
+          transpose_pair(r, even, odd);
+          oe = T::mma(lo, even, T::mma(hi, even, oe));
+          oo = T::mma(lo, odd, T::mma(hi, odd, oo));
+        };
+#pragma unroll
+        for (int d = 0; d < G::kDims; d += 4) {  // 4 dimensions: two words of 16-bit elements
+          uint32_t r0[8], r1[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (E4M3) {
+              r0[i] = T::template from_e4m3<false>(vw[i][d / 4]);
+              r1[i] = T::template from_e4m3<true>(vw[i][d / 4]);
+            } else {
+              r0[i] = vw[i][d / 2];
+              r1[i] = vw[i][d / 2 + 1];
+            }
+          }
+          product(r0, o[d], o[d + 1]);
+          product(r1, o[d + 2], o[d + 3]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (more) load_values(blk + 1);
+      }
+
+      // the four waves' parts, joined: thread (query, col) takes a chunk of the sums
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (grp == 0) stats[wave][col] = make_float2(m, sum);
+      const bool whole = to - from == tokens;
+      float f[kWaves], top = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int piece = 0; piece < G::kEights + G::kFours; ++piece) {
+        const int n = piece < G::kEights ? 8 : 4;
+        __syncthreads();  // the loop's addresses, or the last piece, are read
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              lds.sums[wave][4 * grp + r][col * n + e] = o[8 * piece + e < G::kDims ? 8 * piece + e : 0][r];
+        __syncthreads();
+        if (piece == 0) {
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[w][jq].x);
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            f[w] = stats[w][jq].y == 0.f ? 0.f : __builtin_amdgcn_exp2f(stats[w][jq].x - top);
+            total += f[w] * stats[w][jq].y;
+          }
+        }
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = 0.f;
+          if (e < n)
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) y[e] += f[w] * lds.sums[w][jq][col * n + e];
+        }
+        if (jq >= queries) continue;
+        int d = 128 * piece + n * col;
+        d = d < a.depth - n ? d : a.depth - n;
+        if (whole) {
+          const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[h] : 1.f) / total;
+          uint16_t z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = (uint16_t)T::put(total == 0.f ? 0.f : y[e] * g);
+          char* dst = a.out + b * a.o_row + (head0 + jq) * a.o_head + 2 * d;
+          if (n == 8) __builtin_memcpy(dst, z, 16);
+          else __builtin_memcpy(dst, z, 8);
+          if (piece == 0 && col == 0 && a.lse)
+            a.lse[head] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
+        } else {
+          const int64_t p = (int64_t(head0 + jq) * a.chunks + id) * 2 + (from == 0 ? 1 : 0);
+          float* dst = a.part + p * a.depth + d;
+          if (n == 8) __builtin_memcpy(dst, y, 32);
+          else __builtin_memcpy(dst, y, 16);
+          if (piece == 0 && col == 0) a.stat[p] = make_float2(top, total);
+        }
       }
     }
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = 0.f;
-      if (e < n)
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) y[e] += f[w] * lds.sums[w][jq][col * n + e];
-    }
-    if (jq >= queries) continue;
-    int d = 128 * piece + n * col;
-    d = d < a.depth - n ? d : a.depth - n;
-    if (a.splits == 1) {
-      const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[h] : 1.f) / total;
-      uint16_t z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = (uint16_t)T::put(total == 0.f ? 0.f : y[e] * g);
-      char* dst = a.out + b * a.o_row + (head0 + jq) * a.o_head + 2 * d;
-      if (n == 8) __builtin_memcpy(dst, z, 16);
-      else __builtin_memcpy(dst, z, 8);
-      if (piece == 0 && col == 0 && a.lse)
-        a.lse[head] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
-    } else {
-      const int64_t p = head * a.splits + split;
-      float* dst = a.part + p * a.depth + d;
-      if (n == 8) __builtin_memcpy(dst, y, 32);
-      else __builtin_memcpy(dst, y, 16);
-      if (piece == 0 && col == 0) a.stat[p] = make_float2(top, total);
-    }
+    if (!a.chunks) break;
+    if (before >= t0 && to < tokens) goes_on = make_int2(b, (int)((before + tokens - 1) / share) - (int)id + 1);
+    before += tokens;
+    if (++b == a.rows || (before >= t0 + share && !last)) break;
+    __syncthreads();  // the sums are read
   }
+  if (a.chunks && h == 0 && tile == 0 && threadIdx.x == 0) a.plan[id] = goes_on;
 }
 
-// One workgroup per row and query head: its parts, weighted by their maxima.
-// Wave w takes parts w, w + 4, ..; a lane up to 4 dimensions.
+// One workgroup per chunk and query head: the parts of the row that begins in
+// the chunk and goes on past it, weighted by their maxima.  Wave w takes parts
+// w, w + 4, ..; a lane up to 4 dimensions.
 template <class T>
 __global__ __launch_bounds__(kThreads) void join_kernel(Args a) {
   __shared__ float sums[kWaves][256];
-  __shared__ float2 stats[kWaves];
+  __shared__ float totals[kWaves];
   const int hq = a.heads * a.group;
-  const int b = blockIdx.x / hq, h = blockIdx.x - b * hq;
+  const int chunk = blockIdx.x / hq, h = blockIdx.x - chunk * hq;
+  const int2 plan = a.plan[chunk];
+  const int b = plan.x, parts = plan.y;
+  if (parts == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Range all = attended(a, b);
-  const int share = share_of(a, all), n = all.end - all.begin;
-  const int parts = n > 0 ? (int)((n - 1) / share) + 1 : 1;
-  const float2* stat = a.stat + int64_t(blockIdx.x) * a.splits;
-  const float* part = a.part + int64_t(blockIdx.x) * a.splits * a.depth;
+  const int64_t at = (int64_t(h) * a.chunks + chunk) * 2;
+  const float2* stat = a.stat + at;
+  const float* part = a.part + at * a.depth;
   float top = -INFINITY, total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = lane; i < parts; i += 64) top = fmaxf(top, stat[i].x);
+  for (int i = lane; i < parts; i += 64) top = fmaxf(top, stat[i ? 2 * i : 1].x);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+#pragma unroll 4
   for (int i = wave; i < parts; i += kWaves) {
-    const float2 z = stat[i];
+    const int p = i ? 2 * i : 1;
+    const float2 z = stat[p];
     const float f = z.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(z.x - top);
     total += f * z.y;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int d = lane + 64 * e;
-      if (d < a.depth) y[e] += f * part[int64_t(i) * a.depth + d];
+      if (d < a.depth) y[e] += f * part[int64_t(p) * a.depth + d];
     }
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) sums[wave][lane + 64 * e] = y[e];
-  if (lane == 0) stats[wave].y = total;
+  if (lane == 0) totals[wave] = total;
   __syncthreads();
   total = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) total += stats[w].y;
+  for (int w = 0; w < kWaves; ++w) total += totals[w];
   if ((int)threadIdx.x < a.depth) {
     float all_waves = 0.f;
 #pragma unroll
@@ -576,13 +701,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args a) {
     char* dst = a.out + b * a.o_row + h * a.o_head;
     ((uint16_t*)dst)[threadIdx.x] = (uint16_t)T::put(total == 0.f ? 0.f : all_waves * g);
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[blockIdx.x] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
+  if (threadIdx.x == 0 && a.lse)
+    a.lse[int64_t(b) * hq + h] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
 }
 
 // ---- host -------------------------------------------------------------------
-
-constexpr int64_t kWantGroups = 4096;  // workgroups that fill the chip and balance long against short rows
-constexpr int64_t kLeastShare = 256;   // tokens of a split, at least
 
 int check_query(const char* what, const stg_tensor* t, const char* name) {
   if (int rc = check_tensor(t, name)) return rc;
@@ -593,22 +716,28 @@ int check_query(const char* what, const stg_tensor* t, const char* name) {
   return STG_OK;
 }
 
-// Tokens of a split, from the sizes that the host knows, and how many splits
-// the longest row has.
-struct Split {
-  int64_t share, count;
-};
-Split split_for(int64_t groups, int64_t longest) {
-  if (groups < 1 || longest < 1) return Split{kBlock, 1};
-  const int64_t want = (kWantGroups + groups - 1) / groups;
-  int64_t share = (longest + want - 1) / want;
-  share = share < kLeastShare ? kLeastShare : share;
-  share = (share + kBlock * kWaves - 1) / (kBlock * kWaves) * (kBlock * kWaves);
-  return Split{share, (longest + share - 1) / share};
+// Workgroups that the chip holds at once, by the kernels' registers.
+int64_t resident(int64_t depth, bool e4m3) {
+  return 256 * waves_for((int)(depth + 31) / 32, e4m3);
 }
 
+// Chunks that the rows' tokens are cut into, 0 where each row goes to one
+// workgroup (per cache head and 16 query heads: `heads`).
+// Rows up to this length stay whole: 64 rows of up to 1024 tokens take 33 us so
+// and 37 us cut into chunks; of up to 2000, 61 and 58 (one row of 1200: 19 and 13).
+constexpr int64_t kWholeRows = 1024;
+int64_t chunks_for(int64_t heads, int64_t longest, int64_t room) {
+  if (longest <= kWholeRows || !heads) return 0;
+  // as many workgroups as are resident at once, so that all end together; with
+  // many heads, several times that, so that the last round is a small part
+  const int64_t n = (heads * 8 <= room ? room : 4 * room) / heads;
+  return n < 1 ? 1 : n;
+}
+
+int64_t plan_bytes(int64_t chunks) { return (chunks * 8 + 255) / 256 * 256; }
+
 int plan(const char* what, const stg_tensor* q, const stg_tensor* k_cache, const stg_tensor* page_table, int64_t window,
-         int64_t max_len, int64_t* tiles, Split* split, int64_t* bytes) {
+         int64_t max_len, int64_t* tiles, int64_t* chunks, int64_t* bytes) {
   if (int rc = check_query(what, q, "q")) return rc;
   if (int rc = check_paged_cache(what, k_cache, k_cache, page_table)) return rc;
   const int64_t heads = k_cache->shape[2], depth = q->shape[2];
@@ -623,19 +752,15 @@ int plan(const char* what, const stg_tensor* q, const stg_tensor* k_cache, const
   if (window < 0 || max_len < 0) return fail(STG_ERR_INVALID, "%s: negative window or max_len", what);
   const int64_t group = heads ? q->shape[1] / heads : 0;
   *tiles = (group + kQueries - 1) / kQueries;
-  int64_t groups;
-  if (__builtin_mul_overflow(q->shape[0], heads * *tiles, &groups) || groups > (int64_t(1) << 31) - 1)
-    return fail(STG_ERR_RANGE, "%s: too many rows and heads", what);
   int64_t longest = page_table->shape[1] * k_cache->shape[1];  // each below 2^31
   if (max_len && max_len < longest) longest = max_len;
   if (window && window < longest) longest = window;
-  if (longest > INT32_MAX) longest = INT32_MAX;  // a length is an int32
-  *split = split_for(groups, longest);
-  *bytes = 0;
-  if (split->count > 1) {
-    const int64_t parts = q->shape[0] * q->shape[1] * split->count;
-    *bytes = parts * (8 + depth * 4);
-  }
+  *chunks = chunks_for(heads * *tiles, longest, resident(depth, k_cache->dtype == STG_U8));
+  int64_t groups;
+  if (__builtin_mul_overflow(*chunks ? *chunks : q->shape[0], heads * *tiles, &groups) ||
+      groups > (int64_t(1) << 31) - 1 || *chunks * q->shape[1] > (int64_t(1) << 31) - 1)
+    return fail(STG_ERR_RANGE, "%s: too many rows and heads", what);
+  *bytes = *chunks ? plan_bytes(*chunks) + *chunks * q->shape[1] * 2 * (8 + depth * 4) : 0;
   return STG_OK;
 }
 
@@ -665,9 +790,8 @@ using namespace stg;
 extern "C" int64_t paged_attention_workspace(const stg_tensor* q, const stg_tensor* k_cache,
                                              const stg_tensor* page_table, int64_t window, int64_t max_len) {
   clear_error();
-  int64_t tiles, bytes;
-  Split split;
-  if (int rc = plan("paged_attention_workspace", q, k_cache, page_table, window, max_len, &tiles, &split, &bytes))
+  int64_t tiles, chunks, bytes;
+  if (int rc = plan("paged_attention_workspace", q, k_cache, page_table, window, max_len, &tiles, &chunks, &bytes))
     return -rc;
   return bytes;
 }
@@ -679,9 +803,8 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
                                void* stream) {
   clear_error();
   const char* what = "paged_attention";
-  int64_t tiles, bytes;
-  Split split;
-  if (int rc = plan(what, q, k_cache, page_table, window, max_len, &tiles, &split, &bytes)) return rc;
+  int64_t tiles, chunks, bytes;
+  if (int rc = plan(what, q, k_cache, page_table, window, max_len, &tiles, &chunks, &bytes)) return rc;
   if (int rc = check_paged_cache(what, k_cache, v_cache, page_table)) return rc;
   if (int rc = check_query(what, out, "out")) return rc;
   if (out->dtype != q->dtype) return fail(STG_ERR_INVALID, "%s: out has another dtype than q", what);
@@ -731,16 +854,12 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
   a.group = (int32_t)(q->shape[1] / k_cache->shape[2]);
   a.tiles = (int32_t)tiles;
   a.depth = (int32_t)q->shape[2];
-  a.splits = (int32_t)split.count;
-  a.share = (int32_t)split.share;
+  a.chunks = (int32_t)chunks;
   a.window = window;
-  const int64_t parts = q->shape[0] * q->shape[1] * split.count;
-  a.stat = (float2*)workspace;
-  a.part = (float*)workspace + 2 * parts;
-  int64_t grid;
-  if (__builtin_mul_overflow(int64_t(a.rows) * a.heads * a.tiles, split.count, &grid) || grid > (int64_t(1) << 31) - 1 ||
-      q->shape[0] * q->shape[1] > (int64_t(1) << 31) - 1)
-    return fail(STG_ERR_RANGE, "%s: too many rows and heads", what);
+  a.plan = (int2*)workspace;
+  a.stat = (float2*)((char*)workspace + plan_bytes(chunks));
+  a.part = (float*)(a.stat + chunks * q->shape[1] * 2);
+  const int64_t grid = (chunks ? chunks : q->shape[0]) * a.heads * a.tiles;
   const hipStream_t st = as_stream(stream);
   const bool e4m3 = k_cache->dtype == STG_U8;
   if (q->dtype == STG_BF16) {
@@ -751,9 +870,9 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
     else launch_attention<F16, false>(a, (uint32_t)grid, st);
   }
   if (int rc = check_launch(what)) return rc;
-  if (split.count == 1) return STG_OK;
-  const dim3 rows((uint32_t)(q->shape[0] * q->shape[1]));
-  if (q->dtype == STG_BF16) launch_kernel("paged_attention/join", join_kernel<BF16>, rows, dim3(kThreads), 0, st, a);
-  else launch_kernel("paged_attention/join", join_kernel<F16>, rows, dim3(kThreads), 0, st, a);
+  if (!chunks) return STG_OK;
+  const dim3 joins((uint32_t)(chunks * q->shape[1]));
+  if (q->dtype == STG_BF16) launch_kernel("paged_attention/join", join_kernel<BF16>, joins, dim3(kThreads), 0, st, a);
+  else launch_kernel("paged_attention/join", join_kernel<F16>, joins, dim3(kThreads), 0, st, a);
   return check_launch("paged_attention/join");
 }
