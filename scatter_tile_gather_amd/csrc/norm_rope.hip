@@ -33,7 +33,17 @@ enum CacheKind { kNoCache = 0, kSameCache = 1, kE4m3Cache = 2 };
 struct Rows {  // (tokens, heads, depth), strides in elements
   char* data;
   int64_t token, head;
+  template <class T>
+  __device__ __forceinline__ char* at(int64_t t, int64_t h) const {
+    return data + (t * token + h * head) * T::kBytes;
+  }
 };
+// By value, field by field: a choice between references would put the three
+// into scratch memory.
+__device__ __forceinline__ Rows pick(int role, Rows q, Rows k, Rows v) {
+  return Rows{role == 0 ? q.data : role == 1 ? k.data : v.data, role == 0 ? q.token : role == 1 ? k.token : v.token,
+              role == 0 ? q.head : role == 1 ? k.head : v.head};
+}
 
 struct Turn {
   const float* inv_freq;
@@ -102,66 +112,143 @@ __device__ __forceinline__ void store_one(char* p, float x) {
   else *(uint16_t*)p = (uint16_t)T::put(x);
 }
 
-// n (<= 8, may be <= 0) elements at p; the others are 0.
+// A chunk of 8 elements as it lies in memory.
 template <class T>
-__device__ __forceinline__ void load_chunk(const char* p, int n, float (&x)[8]) {
+struct Raw {
+  uint32_t w[2 * T::kBytes];
+};
+
+// How chunks meet a row's end.
+enum Edge { kWhole = 0, kPart = 1 };  // depth is a multiple of 8; it is not
+
+// Elements [at, at + 8) of a row of `depth` as far as the row goes (n of them;
+// n <= 0: none, and what is read is not used).  A chunk that would pass the
+// row's end is read from further down, so that one load serves any lane and
+// nothing waits for it; unpack() moves it into place.
+template <class T, int EDGE>
+__device__ __forceinline__ void load_raw(const char* row, int at, int n, int depth, Raw<T>& x) {
+  if (EDGE == kWhole || depth >= 8) {
+    const int from = n >= 8 ? at : n <= 0 ? 0 : depth - 8;
+    const char* p = row + from * T::kBytes;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (n >= 8) {
-    if constexpr (T::kBytes == 4) {
-      const u32x4 a = ld16(p), b = ld16(p + 16);
+    for (int i = 0; i < T::kBytes / 2; ++i) {
+      const u32x4 v = ld16(p + 16 * i);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = __uint_as_float(a[i]);
-        x[4 + i] = __uint_as_float(b[i]);
-      }
-    } else {
-      const u32x4 a = ld16(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = T::get(a[i] & 0xFFFFu);
-        x[2 * i + 1] = T::get(a[i] >> 16);
-      }
+      for (int j = 0; j < 4; ++j) x.w[4 * i + j] = v[j];
     }
-  } else {
+  } else {  // fewer than 8 elements: at is 0
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) x[i] = load_one<T>(p + i * T::kBytes);
+    for (int i = 0; i < 2 * T::kBytes; ++i) x.w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      if (i >= n) break;
+      if constexpr (T::kBytes == 4) x.w[i] = *(const uint32_t*)(row + 4 * i);
+      else x.w[i >> 1] |= (uint32_t)*(const uint16_t*)(row + 2 * i) << (16 * (i & 1));
+    }
   }
 }
 
+// Words moved down by `by` (0 .. 7) elements of T, zeros above.
 template <class T>
-__device__ __forceinline__ void store_chunk(char* p, int n, const float (&x)[8]) {
-  if (n >= 8) {
-    if constexpr (T::kBytes == 4) {
-      u32x4 a, b;
+__device__ __forceinline__ void move_down(Raw<T>& x, int by) {
+  constexpr int W = 2 * T::kBytes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = __float_as_uint(x[i]);
-        b[i] = __float_as_uint(x[4 + i]);
-      }
-      st16(p, a);
-      st16(p + 16, b);
+  for (int step = 4; step >= 1; step >>= 1) {
+    const bool on = by & step;
+    if (T::kBytes == 4 || step > 1) {
+      const int d = step * T::kBytes / 4;
+#pragma unroll
+      for (int i = 0; i < W; ++i) x.w[i] = on ? (i + d < W ? x.w[i + d] : 0) : x.w[i];
     } else {
-      u32x4 a;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = T::put(x[2 * i]) | T::put(x[2 * i + 1]) << 16;
-      st16(p, a);
+      for (int i = 0; i < W; ++i) {
+        const uint32_t next = i + 1 < W ? x.w[i + 1] : 0;
+        x.w[i] = on ? x.w[i] >> 16 | next << 16 : x.w[i];
+      }
     }
-  } else {
+  }
+}
+
+template <class T, int EDGE>
+__device__ __forceinline__ void unpack(Raw<T> x, int n, int depth, float (&y)[8]) {
+  if (EDGE == kPart && depth >= 8) move_down<T>(x, n > 0 && n < 8 ? 8 - n : 0);
+#pragma unroll
+  for (int i = 0; i < 2 * T::kBytes; ++i) x.w[i] = n > 0 ? x.w[i] : 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (T::kBytes == 4) y[i] = __uint_as_float(x.w[i]);
+    else y[i] = T::get(i & 1 ? x.w[i >> 1] >> 16 : x.w[i >> 1] & 0xFFFFu);
+  }
+}
+
+// n < 8 elements (none if n <= 0) of BYTES bytes each: the words of x as far
+// as they go, in pieces of 4, 2 and 1.
+template <int BYTES>
+__device__ __forceinline__ void store_part(char* p, int n, const uint32_t* w) {
+  if (n <= 0) return;
+  uint64_t x = w[0] | (uint64_t)w[1] << 32, more = 0;
+  if constexpr (BYTES == 2) more = w[2] | (uint64_t)w[3] << 32;
+  if constexpr (BYTES == 4) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-      if (i < n) store_one<T>(p + i * T::kBytes, x[i]);
+      if (i < n) *(uint32_t*)(p + 4 * i) = w[i];
+  } else {
+    if (n & 4) {
+      __builtin_memcpy(p, &x, 4 * BYTES);
+      p += 4 * BYTES;
+      x = BYTES == 2 ? more : x >> 32;
+    }
+    if (n & 2) {
+      __builtin_memcpy(p, &x, 2 * BYTES);
+      p += 2 * BYTES;
+      x >>= 16 * BYTES;
+    }
+    if (n & 1) __builtin_memcpy(p, &x, BYTES);
   }
+}
+
+template <class T, int EDGE>
+__device__ __forceinline__ void store_chunk(char* p, int n, const float (&x)[8]) {
+  uint32_t w[2 * T::kBytes];
+#pragma unroll
+  for (int i = 0; i < 2 * T::kBytes; ++i) {
+    if constexpr (T::kBytes == 4) w[i] = __float_as_uint(x[i]);
+    else w[i] = T::put(x[2 * i]) | T::put(x[2 * i + 1]) << 16;
+  }
+  if (n >= 8) {
+#pragma unroll
+    for (int i = 0; i < T::kBytes / 2; ++i) st16_nt(p + 16 * i, u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
+  } else if (EDGE == kPart) {
+    store_part<T::kBytes>(p, n, w);
+  }
+}
+
+// A scale and, where that serves, its reciprocal.
+struct Scale {
+  float value, inverse;  // inverse 0: divide
+};
+__device__ __forceinline__ Scale scale_of(float v) {
+  const bool usual = fabsf(v) > 0x1p-100f && fabsf(v) < 0x1p100f;
+  return Scale{v, usual ? 1.f / v : 0.f};
+}
+// x / s rounded to the nearest: the product with the rounded reciprocal, then
+// one step with the exact remainder (Markstein), which large quotients, here
+// only saturated, and infinite ones do not need.
+__device__ __forceinline__ float divided(float x, const Scale& s) {
+  if (s.inverse == 0.f) return x / s.value;
+  const float q = x * s.inverse;
+  const float exact = fmaf(fmaf(-q, s.value, x), s.inverse, q);
+  return fabsf(q) < 1024.f ? exact : q;
 }
 
 // x / scale rounded to the nearest e4m3 code, ties to even, saturated at 448;
 // NaN passes the comparisons and stays NaN.
-__device__ __forceinline__ void store_e4m3(char* p, int n, const float (&x)[8], float scale) {
+template <int EDGE>
+__device__ __forceinline__ void store_e4m3(char* p, int n, const float (&x)[8], const Scale& scale) {
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = x[i] / scale;
+    const float v = divided(x[i], scale);
     y[i] = v > 448.f ? 448.f : v < -448.f ? -448.f : v;
   }
   int w[2];
@@ -172,16 +259,31 @@ __device__ __forceinline__ void store_e4m3(char* p, int n, const float (&x)[8], 
   }
   if (n >= 8) {
     __builtin_memcpy(p, w, 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = (char)(w[i >> 2] >> (8 * (i & 3)));
+  } else if (EDGE == kPart) {
+    const uint32_t u[2] = {(uint32_t)w[0], (uint32_t)w[1]};
+    store_part<1>(p, n, u);
   }
 }
 
-// Sum over the L lanes of a head.
+// Values are computed here and now, so that the registers that they came from
+// are free for loads that follow.
+__device__ __forceinline__ void settle(float (&a)[8], float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(a[i]), "+v"(b[i]));
+}
+
+// Sum over the L lanes of a head: within 16 lanes by DPP.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
 __device__ __forceinline__ float head_sum(float v, int lanes) {
-  for (int d = 1; d < lanes; d <<= 1) v += __shfl_xor(v, d);
+  if (lanes > 1) v += dpp<0xB1>(v);   // lane ^ 1
+  if (lanes > 2) v += dpp<0x4E>(v);   // lane ^ 2
+  if (lanes > 4) v += dpp<0x141>(v);  // 7 - lane: the other four of eight
+  if (lanes > 8) v += dpp<0x140>(v);  // 15 - lane: the other eight of sixteen
+  if (lanes > 16) v += __shfl_xor(v, 16);
+  if (lanes > 32) v += __shfl_xor(v, 32);
   return v;
 }
 
@@ -209,17 +311,21 @@ __device__ __forceinline__ Chunks chunks_of(int sub, int depth, int rotary) {
 }
 
 // cos and sin (times gain) of a token's angles -> cs[0 .. R/2).  position *
-// inv_freq is exact in fp64 up to 2^29 positions and is reduced to one turn
-// there, so fp32 sees an angle of at most pi whatever the position.
+// inv_freq is exact in fp64 up to 2^29 positions and is reduced to a quarter
+// turn there, so fp32 sees an angle of at most pi / 4 whatever the position;
+// from there the Taylor series to r^9 and r^10 leave less than 2^-28.
 __device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float2* cs) {
-  const double kInvTurn = 0.15915494309189533577, kTurnHi = 6.28318530717958623200, kTurnLo = 2.44929359829470641e-16;
+  const double kPerQuarter = 0.63661977236758134308, kQuarterHi = 1.57079632679489655800, kQuarterLo = 6.12323399573676604e-17;
   for (int i = threadIdx.x & 63; i < t.rotary >> 1; i += 64) {
     const double a = (double)position * (double)t.inv_freq[i];
-    const double n = rint(a * kInvTurn);
-    const float r = (float)fma(-n, kTurnLo, fma(-n, kTurnHi, a));
-    float s, c;
-    sincosf(r, &s, &c);
-    cs[i] = make_float2(c * t.gain, s * t.gain);
+    const double n = rint(a * kPerQuarter);
+    const float r = (float)fma(-n, kQuarterLo, fma(-n, kQuarterHi, a));
+    const int quarter = (int)fma(-4.0, floor(n * 0.25), n);
+    const float z = r * r;
+    const float s = fmaf(r * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), r);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+    const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+    cs[i] = make_float2((quarter + 1) & 2 ? -x * t.gain : x * t.gain, quarter & 2 ? -y * t.gain : y * t.gain);
   }
 }
 
@@ -280,116 +386,162 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Chunks&
   }
 }
 
+// A weight (1 where there is none) -> to[0 .. pitch), by the whole workgroup.
 template <class T>
-__device__ __forceinline__ void load_weight(const void* w, int f32, int at, int n, float (&x)[8]) {
-  if (!w) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 1.f;
-  } else if (f32) {
-    load_chunk<F32>((const char*)w + at * 4, n, x);
-  } else {
-    load_chunk<T>((const char*)w + int64_t(at) * T::kBytes, n, x);
+__device__ __forceinline__ void stage_weight(const void* w, int f32, int depth, int pitch, float* to) {
+  for (int d = threadIdx.x; d < pitch; d += kThreads) {
+    float x = 1.f;
+    if (w && d < depth) x = f32 ? ((const float*)w)[d] : load_one<T>((const char*)w + int64_t(d) * T::kBytes);
+    to[d] = x;
   }
 }
 
-// LDS of one wave, in floats: cos and sin of its tokens, then the exchange.
-__host__ __device__ inline int wave_floats(int rotary, int wave_tokens, int mode) {
-  return wave_tokens * rotary + (mode == kHalfExchange ? 1024 : 0);
+// LDS, in floats.  Weights: as many elements as the chunks of L lanes can name.
+__host__ __device__ inline int weight_floats(int lanes) { return lanes * 16 + 8; }
+// One wave's: cos and sin of its tokens, where they go in a cache (keys and
+// values, 64 bits each), the exchange.
+__host__ __device__ inline int wave_floats(int rotary, int wave_tokens, int mode, int cache) {
+  return wave_tokens * (rotary + (cache != kNoCache ? 4 : 0)) + (mode == kHalfExchange ? 1024 : 0);
 }
+
+// The items (token, head) that a group of lanes takes, `step` apart.
+struct Item {
+  int i, h;
+  __device__ __forceinline__ Item(int n, int heads) {
+    i = n / heads;
+    h = n - i * heads;
+  }
+  __device__ __forceinline__ void next(const Item& step, int heads) {
+    i += step.i;
+    h += step.h;
+    if (h >= heads) {
+      h -= heads;
+      ++i;
+    }
+  }
+};
 
 // A wave takes wave_tokens tokens and blockIdx.y's share of their heads; each
 // group of L lanes one head at a time: query heads, then key heads, then (into
-// a cache) value heads.
-template <class T, int MODE, int CACHE>
+// a cache) value heads.  Two heads of a group are on their way while one is
+// computed; the loads are not conditional (past the end they read the first row
+// again), or each would be waited for with the ones after it.
+
+template <class T, int MODE, int CACHE, int EDGE>
 __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows v, const int32_t* positions, Turn t,
                                                            Shape sh, Rows q_out, Rows k_out, Cache cache) {
-  extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float2* cs = (float2*)(lds + wave * wave_floats(t.rotary, sh.wave_tokens, MODE));
-  const int64_t first = (int64_t(blockIdx.x) * kWaves + wave) * sh.wave_tokens;
-  if (first >= sh.tokens) return;
-  const int tokens = sh.tokens - first < sh.wave_tokens ? (int)(sh.tokens - first) : sh.wave_tokens;
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  constexpr int A = 2;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int L = sh.lanes, sub = lane & (L - 1), group = lane / L, groups = 64 / L;
+  const int pitch = weight_floats(L), half = t.rotary >> 1;
+  float* own = lds + 2 * pitch + wave * wave_floats(t.rotary, sh.wave_tokens, MODE, CACHE);
+  int64_t* place = (int64_t*)own;  // of key and value, per token
+  float2* cs = (float2*)(own + (CACHE != kNoCache ? 4 * sh.wave_tokens : 0));
   float* swap = (float*)cs + sh.wave_tokens * t.rotary + group * L * 16;
+  const int64_t first = (int64_t(blockIdx.x) * kWaves + wave) * sh.wave_tokens;
+  const int tokens = first >= sh.tokens ? 0 : sh.tokens - first < sh.wave_tokens ? (int)(sh.tokens - first) : sh.wave_tokens;
   const Chunks c = chunks_of<MODE>(sub, sh.depth, t.rotary);
-  float wqa[8], wqb[8], wka[8], wkb[8];
-  load_weight<T>(t.wq, t.weight_f32, c.a, c.na, wqa);
-  load_weight<T>(t.wq, t.weight_f32, c.b, c.nb, wqb);
-  load_weight<T>(t.wk, t.weight_f32, c.a, c.na, wka);
-  load_weight<T>(t.wk, t.weight_f32, c.b, c.nb, wkb);
-  for (int i = 0; i < tokens; ++i) angles_of(t, positions[first + i], cs + i * (t.rotary >> 1));
-  wave_sync();
   const int heads = sh.q_heads + sh.k_heads * (CACHE == kNoCache ? 1 : 2);
-  for (int item = blockIdx.y * groups + group; item - group < tokens * heads; item += groups * gridDim.y) {
-    const bool live = item < tokens * heads;
-    const int i = live ? item / heads : 0;
-    int h = live ? item - i * heads : 0;
-    const int64_t tok = first + i;
-    const int role = h < sh.q_heads ? 0 : h < sh.q_heads + sh.k_heads ? 1 : 2;
-    h -= role == 0 ? 0 : role == 1 ? sh.q_heads : sh.q_heads + sh.k_heads;
-    const Rows& in = role == 0 ? q : role == 1 ? k : v;
-    const char* src = in.data + (tok * in.token + h * in.head) * T::kBytes;
-    float a[8], b[8];
-    load_chunk<T>(src + int64_t(c.a) * T::kBytes, live ? c.na : 0, a);
-    load_chunk<T>(src + int64_t(c.b) * T::kBytes, live ? c.nb : 0, b);
-    float va[8], vb[8];  // a value's elements pass as they are
-    if constexpr (CACHE != kNoCache) {
+  const int base = blockIdx.y * groups, stride = groups * gridDim.y, total = tokens * heads;
+  const int rounds = total > base ? (total - base + stride - 1) / stride : 0;
+  Item now(base + group, heads), ahead = now;
+  const Item step(stride, heads);
+
+  const auto role_of = [&](int h) { return h < sh.q_heads ? 0 : h < sh.q_heads + sh.k_heads ? 1 : 2; };
+  const auto head_of = [&](int h, int role) {
+    return h - (role == 0 ? 0 : role == 1 ? sh.q_heads : sh.q_heads + sh.k_heads);
+  };
+  Raw<T> ra[A], rb[A];
+  const auto fetch = [&](Raw<T>& a, Raw<T>& b) __attribute__((always_inline)) {
+    const bool live = ahead.i < tokens;
+    const int i = live ? ahead.i : 0, role = live ? role_of(ahead.h) : role_of(0);
+    const char* row = pick(role, q, k, v).at<T>(first + i, live ? head_of(ahead.h, role) : 0);
+    load_raw<T, EDGE>(row, c.a, c.na, sh.depth, a);
+    load_raw<T, EDGE>(row, c.b, c.nb, sh.depth, b);
+    ahead.next(step, heads);
+  };
+  if (rounds) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        va[e] = a[e];
-        vb[e] = b[e];
-      }
-    }
-    if (t.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-      const float r = 1.f / sqrtf(head_sum(ss, L) / (float)sh.depth + t.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] *= r * (role == 0 ? wqa[e] : wka[e]);
-        b[e] *= r * (role == 0 ? wqb[e] : wkb[e]);
-      }
-    }
-    turn<MODE>(a, b, c, cs + i * (t.rotary >> 1), t.rotary, 1.f, swap);
-    if (!live) continue;
-    if (CACHE == kNoCache || role == 0) {
-      const Rows& o = role == 0 ? q_out : k_out;
-      char* dst = o.data + (tok * o.token + h * o.head) * T::kBytes;
-      store_chunk<T>(dst + int64_t(c.a) * T::kBytes, c.na, a);
-      store_chunk<T>(dst + int64_t(c.b) * T::kBytes, c.nb, b);
-      continue;
-    }
-    if constexpr (CACHE != kNoCache) {
-      const int64_t row = cache.token_rows ? cache.token_rows[tok] : tok;
-      const int32_t pos = positions[tok];
-      if (row < 0 || row >= cache.rows || pos < 0) continue;
-      const int32_t entry = pos / cache.slots;
-      if (entry >= cache.width) continue;
-      const int32_t page = cache.table[row * cache.table_stride + entry];
-      if ((uint32_t)page >= (uint32_t)cache.pages) continue;
+    for (int i = 0; i < A; ++i) fetch(ra[i], rb[i]);
+  }
+
+  if (t.norm) {
+    stage_weight<T>(t.wq, t.weight_f32, sh.depth, pitch, lds);
+    stage_weight<T>(t.wk, t.weight_f32, sh.depth, pitch, lds + pitch);
+  }
+  if constexpr (CACHE != kNoCache) {
+    for (int i = lane; i < tokens; i += 64) {
+      const int64_t tok = first + i, row = cache.token_rows ? cache.token_rows[tok] : tok;
+      const int32_t pos = positions[tok], entry = pos / cache.slots;
+      int32_t page = -1;
+      if (row >= 0 && row < cache.rows && pos >= 0 && entry < cache.width)
+        page = cache.table[row * cache.table_stride + entry];
       const int64_t slot = pos - entry * cache.slots;
-      if (role == 2) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] = va[e];
-          b[e] = vb[e];
-        }
-      }
-      const int64_t at = role == 1 ? page * cache.k_page + slot * cache.k_slot + h * cache.k_head
-                                   : page * cache.v_page + slot * cache.v_slot + h * cache.v_head;
-      char* base = role == 1 ? cache.k : cache.v;
-      if constexpr (CACHE == kSameCache) {
-        store_chunk<T>(base + (at + c.a) * T::kBytes, c.na, a);
-        store_chunk<T>(base + (at + c.b) * T::kBytes, c.nb, b);
-      } else {
-        const float* scales = role == 1 ? cache.k_scale : cache.v_scale;
-        const float scale = scales ? scales[h] : 1.f;
-        store_e4m3(base + at + c.a, c.na, a, scale);
-        store_e4m3(base + at + c.b, c.nb, b, scale);
-      }
+      const bool ok = (uint32_t)page < (uint32_t)cache.pages;
+      place[2 * i] = ok ? page * cache.k_page + slot * cache.k_slot : -1;
+      place[2 * i + 1] = ok ? page * cache.v_page + slot * cache.v_slot : -1;
     }
   }
+  for (int i = 0; i < tokens; ++i) angles_of(t, t.rotary ? positions[first + i] : 0, cs + i * half);
+  __syncthreads();
+
+  const float inv_depth = 1.f / (float)sh.depth;
+  const auto compute = [&](Raw<T>& ra, Raw<T>& rb) __attribute__((always_inline)) {
+    const bool live = now.i < tokens;
+    const int role = role_of(now.h), h = head_of(now.h, role), i = live ? now.i : 0;
+    now.next(step, heads);
+    float a[8], b[8];
+    unpack<T, EDGE>(ra, c.na, sh.depth, a);
+    unpack<T, EDGE>(rb, c.nb, sh.depth, b);
+    settle(a, b);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(ra, rb);
+    if (CACHE == kNoCache || role < 2) {
+      if (t.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+        const float r = rsqrtf(head_sum(ss, L) * inv_depth + t.eps);
+        const float* w = lds + (role ? pitch : 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e] *= r * w[c.a + e];
+          b[e] *= r * w[c.b + e];
+        }
+      }
+      turn<MODE>(a, b, c, cs + i * half, t.rotary, 1.f, swap);
+    }
+    if (!live) return;
+    const int64_t tok = first + i;
+    if (CACHE == kNoCache || role == 0) {
+      char* dst = pick(role, q_out, k_out, k_out).at<T>(tok, h);
+      store_chunk<T, EDGE>(dst + int64_t(c.a) * T::kBytes, c.na, a);
+      store_chunk<T, EDGE>(dst + int64_t(c.b) * T::kBytes, c.nb, b);
+      return;
+    }
+    if constexpr (CACHE != kNoCache) {
+      int64_t to = place[2 * i + role - 1];
+      if (to < 0) return;
+      to += h * (role == 1 ? cache.k_head : cache.v_head);
+      char* plane = role == 1 ? cache.k : cache.v;
+      if constexpr (CACHE == kSameCache) {
+        store_chunk<T, EDGE>(plane + (to + c.a) * T::kBytes, c.na, a);
+        store_chunk<T, EDGE>(plane + (to + c.b) * T::kBytes, c.nb, b);
+      } else {
+        const float* scales = role == 1 ? cache.k_scale : cache.v_scale;
+        const Scale scale = scale_of(scales ? scales[h] : 1.f);
+        store_e4m3<EDGE>(plane + to + c.a, c.na, a, scale);
+        store_e4m3<EDGE>(plane + to + c.b, c.nb, b, scale);
+      }
+    }
+  };
+  int round = 0;
+  for (; round + 1 < rounds; round += 2) {
+    compute(ra[0], rb[0]);
+    compute(ra[1], rb[1]);
+  }
+  if (round < rounds) compute(ra[0], rb[0]);
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -404,57 +556,79 @@ struct Gradient {  // queries or keys
 
 // Workgroups 0 .. dq.groups-1 take queries, the others keys; a workgroup's
 // waves walk over its tokens, summing u x' for the weight in registers.
-template <class T, int MODE>
+template <class T, int MODE, int EDGE, bool NORM>
 __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradient dk, const int32_t* positions, Turn t,
                                                             Shape sh) {
-  extern __shared__ float lds[];
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  constexpr int A = T::kBytes == 4 ? 1 : 2;  // heads on their way, as in the forward kernel
   const bool keys = (int)blockIdx.x >= dq.groups;
   const Gradient g = keys ? dk : dq;
   const int group_id = keys ? blockIdx.x - dq.groups : blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float2* cs = (float2*)(lds + wave * wave_floats(t.rotary, sh.wave_tokens, MODE));
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int L = sh.lanes, sub = lane & (L - 1), group = lane / L, groups = 64 / L;
+  const int pitch = weight_floats(L), half = t.rotary >> 1;
+  float2* cs = (float2*)(lds + pitch + wave * wave_floats(t.rotary, sh.wave_tokens, MODE, kNoCache));
   float* swap = (float*)cs + sh.wave_tokens * t.rotary + group * L * 16;
   const Chunks c = chunks_of<MODE>(sub, sh.depth, t.rotary);
-  float wa[8], wb[8], sa[8], sb[8];
-  load_weight<T>(g.w, t.weight_f32, c.a, c.na, wa);
-  load_weight<T>(g.w, t.weight_f32, c.b, c.nb, wb);
+  float sa[8], sb[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sa[e] = sb[e] = 0.f;
+  if (NORM) stage_weight<T>(g.w, t.weight_f32, sh.depth, pitch, lds);
+  __syncthreads();
   const float inv_depth = 1.f / (float)sh.depth;
   for (int64_t first = (int64_t(group_id) * kWaves + wave) * sh.wave_tokens; first < sh.tokens;
        first += int64_t(g.groups) * kWaves * sh.wave_tokens) {
     const int tokens = sh.tokens - first < sh.wave_tokens ? (int)(sh.tokens - first) : sh.wave_tokens;
-    wave_sync();
-    for (int i = 0; i < tokens; ++i) angles_of(t, positions[first + i], cs + i * (t.rotary >> 1));
-    wave_sync();
-    for (int item = group; item - group < tokens * g.heads; item += groups) {
-      const bool live = item < tokens * g.heads;
-      const int i = live ? item / g.heads : 0;
-      const int h = live ? item - i * g.heads : 0;
-      const int64_t tok = first + i;
-      const char* dy = g.dy.data + (tok * g.dy.token + h * g.dy.head) * T::kBytes;
-      float ua[8], ub[8];
-      load_chunk<T>(dy + int64_t(c.a) * T::kBytes, live ? c.na : 0, ua);
-      load_chunk<T>(dy + int64_t(c.b) * T::kBytes, live ? c.nb : 0, ub);
-      float xa[8], xb[8];
-      if (t.norm) {
-        const char* x = g.x.data + (tok * g.x.token + h * g.x.head) * T::kBytes;
-        load_chunk<T>(x + int64_t(c.a) * T::kBytes, live ? c.na : 0, xa);
-        load_chunk<T>(x + int64_t(c.b) * T::kBytes, live ? c.nb : 0, xb);
+    const int total = tokens * g.heads, rounds = (total + groups - 1) / groups;
+    if (!rounds) break;  // no heads
+    Item now(group, g.heads), ahead = now;
+    const Item step(groups, g.heads);
+    Raw<T> ya[A], yb[A], va[A], vb[A];
+    const auto fetch = [&](int slot) __attribute__((always_inline)) {
+      const bool live = ahead.i < tokens;
+      const int64_t tok = first + (live ? ahead.i : 0), h = live ? ahead.h : 0;
+      const char* dy = g.dy.template at<T>(tok, h);
+      load_raw<T, EDGE>(dy, c.a, c.na, sh.depth, ya[slot]);
+      load_raw<T, EDGE>(dy, c.b, c.nb, sh.depth, yb[slot]);
+      if (NORM) {
+        const char* x = g.x.template at<T>(tok, h);
+        load_raw<T, EDGE>(x, c.a, c.na, sh.depth, va[slot]);
+        load_raw<T, EDGE>(x, c.b, c.nb, sh.depth, vb[slot]);
       }
-      turn<MODE>(ua, ub, c, cs + i * (t.rotary >> 1), t.rotary, -1.f, swap);
-      if (t.norm) {
+      ahead.next(step, g.heads);
+    };
+#pragma unroll
+    for (int i = 0; i < A; ++i) fetch(i);
+    wave_sync();
+    for (int i = 0; i < tokens; ++i) angles_of(t, t.rotary ? positions[first + i] : 0, cs + i * half);
+    wave_sync();
+    const auto compute = [&](int slot) __attribute__((always_inline)) {
+      const bool live = now.i < tokens;
+      const int i = live ? now.i : 0, h = now.h;
+      now.next(step, g.heads);
+      float ua[8], ub[8], xa[8], xb[8];
+      unpack<T, EDGE>(ya[slot], c.na, sh.depth, ua);
+      unpack<T, EDGE>(yb[slot], c.nb, sh.depth, ub);
+      if (NORM) {
+        unpack<T, EDGE>(va[slot], c.na, sh.depth, xa);
+        unpack<T, EDGE>(vb[slot], c.nb, sh.depth, xb);
+      }
+      settle(ua, ub);
+      if (NORM) settle(xa, xb);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(slot);
+      turn<MODE>(ua, ub, c, cs + i * half, t.rotary, -1.f, swap);
+      if (NORM) {
         // with r = 1 / sqrt(mean(x^2) + eps): dx = r u w - x r^3 mean(u w x)
         float ss = 0.f, sd = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           ss += xa[e] * xa[e] + xb[e] * xb[e];
-          sd += ua[e] * wa[e] * xa[e] + ub[e] * wb[e] * xb[e];
+          sd += ua[e] * lds[c.a + e] * xa[e] + ub[e] * lds[c.b + e] * xb[e];
         }
         ss = head_sum(ss, L);
         sd = head_sum(sd, L);
-        const float r = 1.f / sqrtf(ss * inv_depth + t.eps);
+        const float r = rsqrtf(ss * inv_depth + t.eps);
         const float back = r * sd * inv_depth;  // mean(u w x')
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -464,16 +638,22 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
             sa[e] += ua[e] * xa[e];
             sb[e] += ub[e] * xb[e];
           }
-          ua[e] = r * (ua[e] * wa[e] - xa[e] * back);
-          ub[e] = r * (ub[e] * wb[e] - xb[e] * back);
+          ua[e] = r * (ua[e] * lds[c.a + e] - xa[e] * back);
+          ub[e] = r * (ub[e] * lds[c.b + e] - xb[e] * back);
         }
       }
       if (live) {
-        char* dx = g.dx.data + (tok * g.dx.token + h * g.dx.head) * T::kBytes;
-        store_chunk<T>(dx + int64_t(c.a) * T::kBytes, c.na, ua);
-        store_chunk<T>(dx + int64_t(c.b) * T::kBytes, c.nb, ub);
+        char* dx = g.dx.template at<T>(first + i, h);
+        store_chunk<T, EDGE>(dx + int64_t(c.a) * T::kBytes, c.na, ua);
+        store_chunk<T, EDGE>(dx + int64_t(c.b) * T::kBytes, c.nb, ub);
       }
+    };
+    int round = 0;
+    for (; round + A <= rounds; round += A) {
+      compute(0);
+      if (A > 1) compute(A > 1 ? 1 : 0);
     }
+    if (A > 1 && round < rounds) compute(0);
   }
   if (!g.partial) return;  // the same for all waves of the workgroup
   for (int d = L; d < 64; d <<= 1) {
@@ -483,7 +663,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
       sb[e] += __shfl_xor(sb[e], d);
     }
   }
-  __syncthreads();  // LDS is free of angles
+  __syncthreads();  // LDS is free of weights and angles
   if (group == 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -595,6 +775,11 @@ void with_mode(int mode, F&& f) {
   else f(std::integral_constant<int, kHalfExchange>{});
 }
 template <class F>
+void with_edge(int32_t depth, F&& f) {
+  if (depth % 8 == 0) f(std::integral_constant<int, kWhole>{});
+  else f(std::integral_constant<int, kPart>{});
+}
+template <class F>
 void with_type(int32_t dtype, F&& f) {
   if (dtype == STG_BF16) f(BF16{});
   else if (dtype == STG_F16) f(F16{});
@@ -627,13 +812,16 @@ int launch_forward(const char* what, int32_t dtype, int mode, const Rows& q, con
   int shares = 1;
   while (shares < rounds && blocks * kWaves * shares < 1024) shares *= 2;
   const dim3 grid((uint32_t)blocks, (uint32_t)(shares < rounds ? shares : rounds));
-  const uint32_t shmem = kWaves * wave_floats(t.rotary, sh.wave_tokens, mode) * 4;
+  const uint32_t shmem =
+      (2 * weight_floats(sh.lanes) + kWaves * wave_floats(t.rotary, sh.wave_tokens, mode, CACHE)) * 4;
   with_type(dtype, [&](auto type) {
     with_mode(mode, [&](auto m) {
       using T = decltype(type);
       if constexpr (CACHE == kNoCache || T::kBytes == 2)
-        launch_kernel(what, forward_kernel<T, decltype(m)::value, CACHE>, grid, dim3(kThreads), shmem, st, q, k, v,
-                      positions, t, sh, q_out, k_out, cache);
+        with_edge(sh.depth, [&](auto e) {
+          launch_kernel(what, forward_kernel<T, decltype(m)::value, CACHE, decltype(e)::value>, grid, dim3(kThreads),
+                        shmem, st, q, k, v, positions, t, sh, q_out, k_out, cache);
+        });
     });
   });
   return check_launch(what);
@@ -806,13 +994,18 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
   const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, dq_weight ? pq : nullptr};
   const Gradient gk{rows_of(dk_out), rows_of(k), rows_of(dk), t.wk, sh.k_heads, nk, dk_weight ? pk : nullptr};
   const hipStream_t st = as_stream(stream);
-  uint32_t shmem = kWaves * wave_floats(t.rotary, sh.wave_tokens, mode) * 4;
+  uint32_t shmem = (weight_floats(sh.lanes) + kWaves * wave_floats(t.rotary, sh.wave_tokens, mode, kNoCache)) * 4;
   if (shmem < kWaves * (uint32_t)sh.depth * 4) shmem = kWaves * sh.depth * 4;
   if (!sh.tokens && !sums) return STG_OK;
   with_type(q->dtype, [&](auto type) {
     with_mode(mode, [&](auto m) {
-      launch_kernel(what, backward_kernel<decltype(type), decltype(m)::value>, dim3(nq + nk), dim3(kThreads), shmem, st,
-                    gq, gk, positions, t, sh);
+      with_edge(sh.depth, [&](auto e) {
+        const auto go = [&](auto kernel) {
+          launch_kernel(what, kernel, dim3(nq + nk), dim3(kThreads), shmem, st, gq, gk, positions, t, sh);
+        };
+        if (t.norm) go(backward_kernel<decltype(type), decltype(m)::value, decltype(e)::value, true>);
+        else go(backward_kernel<decltype(type), decltype(m)::value, decltype(e)::value, false>);
+      });
     });
   });
   if (int rc = check_launch(what)) return rc;
