@@ -554,8 +554,10 @@ struct Gradient {  // queries or keys
   float* partial;   // (groups, depth) or null
 };
 
-// Workgroups 0 .. dq.groups-1 take queries, the others keys; a workgroup's
-// waves walk over its tokens, summing u x' for the weight in registers.
+// Workgroups 0 .. dq.groups-1 take queries, the others keys.  A wave has a run
+// of tokens and walks over their heads, summing u x' for the weight in
+// registers; loads are ahead as in the forward kernel, for the whole run, and
+// the angles of wave_tokens tokens are computed as the walk reaches them.
 template <class T, int MODE, int EDGE, bool NORM>
 __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradient dk, const int32_t* positions, Turn t,
                                                             Shape sh) {
@@ -576,13 +578,15 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
   if (NORM) stage_weight<T>(g.w, t.weight_f32, sh.depth, pitch, lds);
   __syncthreads();
   const float inv_depth = 1.f / (float)sh.depth;
-  for (int64_t first = (int64_t(group_id) * kWaves + wave) * sh.wave_tokens; first < sh.tokens;
-       first += int64_t(g.groups) * kWaves * sh.wave_tokens) {
-    const int tokens = sh.tokens - first < sh.wave_tokens ? (int)(sh.tokens - first) : sh.wave_tokens;
-    const int total = tokens * g.heads, rounds = (total + groups - 1) / groups;
-    if (!rounds) break;  // no heads
+  const int64_t run = (sh.tokens + int64_t(g.groups) * kWaves - 1) / (int64_t(g.groups) * kWaves);
+  const int64_t first = (int64_t(group_id) * kWaves + wave) * run, left = sh.tokens - first;
+  const int tokens = (int)(left < 0 ? 0 : left < run ? left : run);
+  const int total = tokens * g.heads, rounds = (total + groups - 1) / groups;
+  if (rounds) {
     Item now(group, g.heads), ahead = now;
     const Item step(groups, g.heads);
+    Item lead(0, g.heads), tail(groups - 1, g.heads);  // of a round: its first item and its last
+    int block = 0, covered = 0;                        // tokens whose angles are in LDS: [block, covered)
     Raw<T> ya[A], yb[A], va[A], vb[A];
     const auto fetch = [&](int slot) __attribute__((always_inline)) {
       const bool live = ahead.i < tokens;
@@ -599,13 +603,21 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
     };
 #pragma unroll
     for (int i = 0; i < A; ++i) fetch(i);
-    wave_sync();
-    for (int i = 0; i < tokens; ++i) angles_of(t, t.rotary ? positions[first + i] : 0, cs + i * half);
-    wave_sync();
     const auto compute = [&](int slot) __attribute__((always_inline)) {
+      const int need = tail.i < tokens ? tail.i : tokens - 1;
+      if (need >= covered) {
+        block = lead.i;
+        covered = block + sh.wave_tokens < tokens ? block + sh.wave_tokens : tokens;
+        wave_sync();
+        if (half)
+          for (int i = block; i < covered; ++i) angles_of(t, positions[first + i], cs + (i - block) * half);
+        wave_sync();
+      }
       const bool live = now.i < tokens;
-      const int i = live ? now.i : 0, h = now.h;
+      const int i = live ? now.i : lead.i, h = now.h;
       now.next(step, g.heads);
+      lead.next(step, g.heads);
+      tail.next(step, g.heads);
       float ua[8], ub[8], xa[8], xb[8];
       unpack<T, EDGE>(ya[slot], c.na, sh.depth, ua);
       unpack<T, EDGE>(yb[slot], c.nb, sh.depth, ub);
@@ -617,7 +629,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
       if (NORM) settle(xa, xb);
       __builtin_amdgcn_sched_barrier(0);
       fetch(slot);
-      turn<MODE>(ua, ub, c, cs + i * half, t.rotary, -1.f, swap);
+      turn<MODE>(ua, ub, c, cs + (i - block) * half, t.rotary, -1.f, swap);
       if (NORM) {
         // with r = 1 / sqrt(mean(x^2) + eps): dx = r u w - x r^3 mean(u w x)
         float ss = 0.f, sd = 0.f;
@@ -693,6 +705,7 @@ __global__ __launch_bounds__(1024) void weight_kernel(const float* pq, int nq, v
   const int col = threadIdx.x & 63, row = threadIdx.x >> 6, d = blockIdx.x * 64 + col;
   float s = 0.f;
   if (d < depth)
+#pragma unroll 8
     for (int i = row; i < n; i += 16) s += p[int64_t(i) * depth + d];
   sums[row][col] = s;
   __syncthreads();
@@ -827,21 +840,34 @@ int launch_forward(const char* what, int32_t dtype, int mode, const Rows& q, con
   return check_launch(what);
 }
 
-// Workgroups that sum a weight gradient: enough to fill the chip, each with
-// a few tokens at least.
-int32_t sum_groups(int64_t tokens, int32_t wave_tokens, int64_t most) {
-  const int64_t n = (tokens + int64_t(kWaves) * wave_tokens - 1) / (int64_t(kWaves) * wave_tokens);
+// Tokens whose angles a wave of the backward has at a time: what one round can
+// touch, and 4 KiB of them where that is more.
+int32_t backward_tokens(const Shape& sh, int rotary) {
+  const int groups = 64 / sh.lanes;
+  int heads = sh.q_heads;
+  if (!heads || (sh.k_heads && sh.k_heads < heads)) heads = sh.k_heads;
+  const int touched = groups == 1 || !heads ? 1 : (groups - 1) / heads + 2;
+  const int n = rotary ? 1024 / rotary : 8;
+  return touched > n ? touched : n < 8 ? n : touched > 8 ? touched : 8;
+}
+
+// Workgroups of the backward: as many as the chip holds at once (by its
+// registers, 3 waves a SIMD with the norm, 5 without), shared out between
+// queries and keys by their heads; fewer where waves would not have a head for
+// each of their groups of lanes.
+constexpr int64_t kSumGroups = 1536, kTurnGroups = 1280;
+int32_t groups_for(const Shape& sh, int64_t heads, int64_t most) {
+  if (!heads) return 1;
+  const int64_t per_wave = (64 / sh.lanes + heads - 1) / heads;  // tokens
+  const int64_t n = (sh.tokens + kWaves * per_wave - 1) / (kWaves * per_wave);
   return (int32_t)(n < 1 ? 1 : n > most ? most : n);
 }
-constexpr int64_t kSumGroups = 1024;
-
-// (query workgroups, key workgroups): shared out by heads
-void split_groups(const Shape& sh, int32_t* nq, int32_t* nk) {
-  const int64_t heads = sh.q_heads + sh.k_heads;
-  int64_t q = heads ? kSumGroups * sh.q_heads / heads : 0;
-  q = q < 1 ? 1 : q > kSumGroups - 1 ? kSumGroups - 1 : q;
-  *nq = sum_groups(sh.tokens, sh.wave_tokens, q);
-  *nk = sum_groups(sh.tokens, sh.wave_tokens, kSumGroups - q);
+void split_groups(const Shape& sh, bool norm, int32_t* nq, int32_t* nk) {
+  const int64_t all = norm ? kSumGroups : kTurnGroups, heads = sh.q_heads + sh.k_heads;
+  int64_t q = heads ? all * sh.q_heads / heads : 0;
+  q = q < 1 ? 1 : q > all - 1 ? all - 1 : q;
+  *nq = groups_for(sh, sh.q_heads, q);
+  *nk = groups_for(sh, sh.k_heads, all - q);
 }
 
 }  // namespace
@@ -984,11 +1010,9 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
       return fail(STG_ERR_INVALID, "%s: needs a workspace of %lld bytes", what, (long long)need);
     if ((uintptr_t)workspace & 255) return fail(STG_ERR_INVALID, "%s: workspace must be 256-byte aligned", what);
   }
-  const int heads = sh.q_heads < sh.k_heads ? sh.q_heads : sh.k_heads;
-  sh.wave_tokens = wave_tokens_for(sh, heads, t.rotary);
-  while (sh.wave_tokens > 1 && sh.tokens < 1024 * sh.wave_tokens) sh.wave_tokens = (sh.wave_tokens + 1) / 2;
+  sh.wave_tokens = backward_tokens(sh, t.rotary);
   int32_t nq, nk;
-  split_groups(sh, &nq, &nk);
+  split_groups(sh, t.norm, &nq, &nk);
   float* pq = (float*)workspace;
   float* pk = pq + int64_t(nq) * sh.depth;
   const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, dq_weight ? pq : nullptr};
