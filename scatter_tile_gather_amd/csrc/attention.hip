@@ -164,12 +164,13 @@ __device__ __forceinline__ void wave_sync() {
 
 __device__ __forceinline__ void put_words(uint32_t* w, u32x4 x) { w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3]; }
 __device__ __forceinline__ void put_words(uint32_t* w, u32x2 x) { w[0] = x[0], w[1] = x[1]; }
-// At any alignment; NT: non-temporal.
+// From an address in global memory, at any alignment; NT: non-temporal.
 template <class V, bool NT>
-__device__ __forceinline__ V load_as(const char* p) {
+__device__ __forceinline__ V load_as(int64_t address) {
   typedef V any __attribute__((aligned(1)));
-  if constexpr (NT) return __builtin_nontemporal_load((const any*)p);
-  else return *(const any*)p;
+  const auto* p = (const __attribute__((address_space(1))) any*)address;
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
 }
 
 // DS: depth in steps of 32 (rounded up); E4M3: the caches hold e4m3 codes;
@@ -263,6 +264,7 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
   __shared__ union {
     struct {
       int64_t k[kWaves][2][kSpan], v[kWaves][2][kSpan];
+      __attribute__((aligned(8))) uint32_t there[kWaves][2][kSpanBlocks];  // a bit per token
       __attribute__((aligned(16))) char keys[kWaves][G::kTile];
     } at;
     float sums[kWaves][kQueries][128];
@@ -352,9 +354,9 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
       from = before < t0 ? (int)(t0 - before) : 0;
       to = before + tokens > t0 + share ? (int)(t0 + share - before) : tokens;
     }
-    const int jq = thread >> 4;
-    const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
     if (tokens == 0) {
+      const int jq = thread >> 4;
+      const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
       if (jq < queries) {
         uint16_t* dst = (uint16_t*)(a.out + b * a.o_row + (head0 + jq) * a.o_head);
         for (int d = col; d < a.depth; d += 16) dst[d] = 0;
@@ -379,7 +381,6 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
         }
       }
 
-      const char* kbase = a.k + h * a.k_head;
       int key_row[G::kPeriod], key_from[G::kPeriod], key_to[G::kPeriod];
 #pragma unroll
       for (int i = 0; i < G::kPeriod; ++i) {
@@ -389,30 +390,27 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
         key_from[i] = G::chunk_from(chunk, a.depth) * kElem;
         key_to[i] = key_row[i] * G::kPitch + chunk * G::kChunk;
       }
-      const char* vbase = a.v + h * a.v_head + (G::kExact ? (G::kEights ? 8 : 4) * col * kElem : 0);
-      // where this lane's chunks begin, from those bases
       const auto value8_at = [&](int i) {
         const int d = 128 * i + 8 * col;
-        return (G::kExact ? 128 * i : d < a.depth - 8 ? d : a.depth - 8) * kElem;
+        return (G::kExact || d < a.depth - 8 ? d : a.depth - 8) * kElem;
       };
       const auto value4_at = [&]() {
         const int d = 128 * G::kEights + 4 * col;
-        return (G::kExact ? (G::kEights ? d - 8 * col : 0) : d < a.depth - 4 ? d : a.depth - 4) * kElem;
+        return (G::kExact || d < a.depth - 4 ? d : a.depth - 4) * kElem;
       };
 
       // A span's addresses: its pages are loaded a span ahead, its offsets go to
-      // LDS when the loop reaches it.  A token without a page has offset 0, which
-      // may be read, and a zero in `there`.
+      // LDS when the loop reaches it.  A token without a page has the first row's
+      // address, which may be read, and a zero in `there`.
       int32_t page[2];
-      const auto fetch = [&](int span) {
+      const auto fetch = [&](int span) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int i = span * kSpan + 64 * t + lane;
           page[t] = i < n ? a.table[b * a.table_stride + (begin + i) / (uint32_t)a.slots] : -1;
         }
       };
-      uint64_t there[2];
-      const auto place = [&](int span) {
+      const auto place = [&](int span) __attribute__((always_inline)) {
         int64_t* k = lds.at.k[wave][span & 1];
         int64_t* v = lds.at.v[wave][span & 1];
 #pragma unroll
@@ -420,9 +418,10 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
           const uint32_t j = begin + span * kSpan + 64 * t + lane;
           const int64_t slot = j % (uint32_t)a.slots;
           const bool ok = (uint32_t)page[t] < (uint32_t)a.pages;
-          k[64 * t + lane] = ok ? page[t] * a.k_page + slot * a.k_slot : 0;
-          v[64 * t + lane] = ok ? page[t] * a.v_page + slot * a.v_slot : 0;
-          there[t] = __ballot(ok);
+          k[64 * t + lane] = (int64_t)a.k + h * a.k_head + (ok ? page[t] * a.k_page + slot * a.k_slot : 0);
+          v[64 * t + lane] = (int64_t)a.v + h * a.v_head + (ok ? page[t] * a.v_page + slot * a.v_slot : 0);
+          const uint64_t all_ok = __ballot(ok);
+          if (lane == 0) *(uint64_t*)&lds.at.there[wave][span & 1][2 * t] = all_ok;
         }
         wave_sync();
       };
@@ -431,16 +430,16 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
       using value_vec = std::conditional_t<E4M3, u32x2, u32x4>;  // 8 elements
       chunk_vec kv[G::kLoads];          // the block's keys on their way to LDS
       uint32_t vw[8][G::kValueWords];   // values of tokens 4 grp + i, 12 + 4 grp + i (i >= 4)
-      const auto load_keys = [&](int blk) {
+      const auto load_keys = [&](int blk) __attribute__((always_inline)) {
         const int64_t* k = &lds.at.k[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
 #pragma unroll
         for (int i = 0; i < G::kLoads; ++i) {
           const int j = i % G::kPeriod;
-          kv[i] = load_as<chunk_vec, G::kLines>(kbase + k[key_row[j] + i / G::kPeriod * G::kRows] + key_from[j]);
+          kv[i] = load_as<chunk_vec, G::kLines>(k[key_row[j] + i / G::kPeriod * G::kRows] + key_from[j]);
         }
       };
       char* const keys = lds.at.keys[wave];
-      const auto store_keys = [&]() {
+      const auto store_keys = [&]() __attribute__((always_inline)) {
         wave_sync();  // the block before is read
 #pragma unroll
         for (int i = 0; i < G::kLoads; ++i)
@@ -448,17 +447,17 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
         wave_sync();
       };
       // 8 elements of token 16 t + col
-      const auto key_words = [&](int t, int st) {
+      const auto key_words = [&](int t, int st) __attribute__((always_inline)) {
         const char* row = keys + (16 * t + col) * G::kPitch;
         if constexpr (!E4M3) return *(const u32x4*)(row + (4 * st + grp) * 16);
         else if constexpr (RAGGED) return *(const u32x2*)(row + (4 * st + grp) * 8);
         else return *(const u32x2*)(row + G::dim(st, grp));
       };
-      const auto load_values = [&](int blk) {
+      const auto load_values = [&](int blk) __attribute__((always_inline)) {
         const int64_t* v = &lds.at.v[wave][blk / kSpanBlocks & 1][blk % kSpanBlocks * kBlock];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const char* row = vbase + v[16 * (i >> 2) + 4 * grp + (i & 3)];
+          const int64_t row = v[16 * (i >> 2) + 4 * grp + (i & 3)];
           uint32_t* w = vw[i];
 #pragma unroll
           for (int g = 0; g < G::kEights; ++g) {
@@ -477,27 +476,13 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
       for (int e = 0; e < G::kDims; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
       m = -INFINITY;
       sum = 0.f;
-      // (set where no block follows, so that nothing lives on from the row before)
-#pragma unroll
-      for (int i = 0; i < G::kLoads; ++i) kv[i] = chunk_vec{};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int w = 0; w < G::kValueWords; ++w) vw[i][w] = 0;
-      page[0] = page[1] = -1;
-      there[0] = there[1] = 0;
-      if (blocks > 0) {
-        fetch(0);
-        place(0);
-        if (blocks > kSpanBlocks) fetch(1);
-        load_keys(0);
-        load_values(0);
-      }
-      for (int blk = 0; blk < blocks; ++blk) {
+      // The last block is computed apart: were the loads of the next one
+      // conditional, every wait would be for all loads.
+      const auto compute = [&](int blk, auto has_next) __attribute__((always_inline)) {
+        constexpr bool more = decltype(has_next)::value;
         const int in_span = blk % kSpanBlocks;
-        const uint64_t pair = in_span & 2 ? there[1] : there[0];
-        const uint32_t here = in_span & 1 ? (uint32_t)(pair >> 32) : (uint32_t)pair;
-        const bool more = blk + 1 < blocks;
+        const uint32_t here =
+            __builtin_amdgcn_readfirstlane(lds.at.there[wave][blk / kSpanBlocks & 1][in_span]);
         if (in_span == kSpanBlocks - 1 && more) {
           const int span = blk / kSpanBlocks + 1;
           place(span);
@@ -563,7 +548,7 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
             for (int w = 0; w < G::kValueWords; ++w)
               if (!(mine >> (16 * (i >> 2) + (i & 3)) & 1)) vw[i][w] = 0;
         }
-        const auto product = [&](const uint32_t(&r)[8], f32x4& oe, f32x4& oo) {
+        const auto product = [&](const uint32_t(&r)[8], f32x4& oe, f32x4& oo) __attribute__((always_inline)) {
           u32x4 even, odd;
           transpose_pair(r, even, odd);
           oe = T::mma(lo, even, T::mma(hi, even, oe));
@@ -587,6 +572,18 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
           __builtin_amdgcn_sched_barrier(0);
         }
         if (more) load_values(blk + 1);
+      };
+      if (blocks > 0) {
+        fetch(0);
+        place(0);
+        // the queries have arrived, and the loop need not look for them among its loads
+#pragma unroll
+        for (int st = 0; st < DS; ++st) asm volatile("" : "+v"(qf[st]));
+        if (blocks > kSpanBlocks) fetch(1);
+        load_keys(0);
+        load_values(0);
+        for (int blk = 0; blk + 1 < blocks; ++blk) compute(blk, std::true_type{});
+        compute(blocks - 1, std::false_type{});
       }
 
       // the four waves' parts, joined: thread (query, col) takes a chunk of the sums
@@ -594,6 +591,8 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
       sum += __shfl_xor(sum, 32);
       if (grp == 0) stats[wave][col] = make_float2(m, sum);
       const bool whole = to - from == tokens;
+      const int jq = thread >> 4;
+      const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
       float f[kWaves], top = -INFINITY, total = 0.f;
 #pragma unroll
       for (int piece = 0; piece < G::kEights + G::kFours; ++piece) {
