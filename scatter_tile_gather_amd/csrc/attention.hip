@@ -7,10 +7,11 @@
 //    longer ones the tokens of all rows, end to end, are cut into as many equal
 //    chunks as the chip holds workgroups, so that all end together however
 //    ragged the rows are, and a second kernel joins the rows that were cut.
-//    64 rows of 1 .. 8192 tokens, 8 heads of 128, bf16: 183 us (6.0 TB/s of keys
-//    and values); cut row by row into parts of 1024 tokens: 201 us.
-//  - Its four waves each take a quarter of a row's tokens and walk over blocks
-//    of 32.  A block's keys and values are loaded into registers while the
+//    64 rows of 1 .. 8192 tokens, 8 heads of 128, bf16: 173 us (6.3 TB/s of keys
+//    and values, where a kernel that only reads rows of 256 bytes so reaches 6.7
+//    to 7.1); cut row by row into parts of 1024 tokens it took 18 us more.
+//  - Its four waves each take a quarter of a row's tokens (or half of them for
+//    one of two neighbouring heads, see pays_as_pair) and walk over blocks of 32.  A block's keys and values are loaded into registers while the
 //    block before is computed; its addresses come from LDS, a span of 128
 //    tokens ahead.  There is no barrier in the loop.
 //  - Scores are computed transposed, S^T = K Q^T (v_mfma 16x16x32): a lane then
@@ -21,14 +22,14 @@
 //    them in any order as long as V is fed in the same one.
 //  - Loads cover whole rows, 256 contiguous bytes in 16 lanes: read as matrix
 //    operands straight away, K would come in pieces of 64 bytes of 16 rows, and
-//    that costs a seventh (231 us instead of 201 above).  K's rows become operands
-//    through LDS.  V is wanted with 8 tokens of one dimension in a lane but lies
+//    that cost a seventh.  K's rows become operands through LDS.  V is wanted with 8 tokens of one dimension in a lane but lies
 //    with 8 dimensions of one token in 16 bytes: a lane loads 8 x 8 elements and
 //    transposes them with byte permutes in its own registers.
-//  - Where rows are whole cache lines, loads are non-temporal (224 us without).
+//  - Where rows are whole cache lines, loads are non-temporal (an eighth faster).
 //    Where they are not, neighbouring heads share lines: then the heads of a
 //    token run on one XCD, whose L2 keeps the line for the next (depth 100,
-//    64 rows of up to 4096 tokens: 109 us; non-temporal and spread over XCDs 138).
+//    64 rows of up to 4096 tokens: 102 us; a quarter more if non-temporal and
+//    spread over the XCDs).
 //  - One pass, with a running maximum that is raised only when a score exceeds
 //    it by a margin (kRaise): the usual iteration needs no exchange between
 //    lanes and no rescaling.
@@ -69,10 +70,12 @@ struct Args {
   // that begins in the chunk and goes on past it, the first for one from before
   float* part;   // .. of depth: sums relative to the part's maximum
   float2* stat;  // maximum (log2) and sum
-  int2* plan;    // per chunk: the row that begins in it and goes on, and over how many chunks
+  int2* plan;    // by_row, per row: the chunk that it begins in, and over how many it goes (0: one);
+                 // else per chunk: the row that begins in it and goes on, and over how many (0: none)
   float scale_log2;
   int32_t rows, width, pages, slots;
   int32_t heads, group, tiles, depth;
+  int32_t by_row;
   int32_t chunks;  // 0: a workgroup takes a row; else the rows' tokens, end to end, are cut into this many
   int64_t window;
 };
@@ -255,7 +258,8 @@ __device__ __forceinline__ void transpose_pair(const uint32_t (&r)[8], u32x4& ev
 // Waves of a SIMD that the registers are shared out to.
 constexpr int waves_for(int ds, bool e4m3) { return ds <= 2 ? 4 : ds <= 4 ? 3 : ds <= 6 || e4m3 ? 2 : 1; }
 
-template <class T, int DS, bool E4M3, bool RAGGED>
+// PAIR: a workgroup takes two neighbouring cache heads, two waves each.
+template <class T, int DS, bool E4M3, bool RAGGED, bool PAIR>
 __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention_kernel(Args a) {
   using G = Geometry<T, DS, E4M3, RAGGED>;
   constexpr int kElem = E4M3 ? 1 : 2;
@@ -272,8 +276,9 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
   __shared__ float2 stats[kWaves][kQueries];
 
   uint32_t id = G::kLines ? blockIdx.x : xcd_remap(blockIdx.x, gridDim.x);
-  const int h = id % a.heads;
-  id /= a.heads;
+  constexpr int pair = PAIR ? 1 : 0;
+  const int h0 = id % (a.heads >> pair) << pair;  // the first, or only, cache head
+  id /= a.heads >> pair;
   const int tile = id % a.tiles;
   id /= a.tiles;
   // A workgroup's tokens: row id, or chunk id of all rows' tokens end to end,
@@ -314,7 +319,7 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
     t0 = id * share;
     last = t0 + share >= total;
     if (id > 0 && t0 >= total) {
-      if (h == 0 && tile == 0 && threadIdx.x == 0) a.plan[id] = make_int2(-1, 0);
+      if (!a.by_row && h0 == 0 && tile == 0 && threadIdx.x == 0) a.plan[id] = make_int2(-1, 0);
       return;
     }
     int first = a.rows;
@@ -335,16 +340,14 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
   }
   int2 goes_on = make_int2(-1, 0);
 
-  const int head0 = h * a.group + tile * kQueries;
   const int queries = a.group - tile * kQueries < kQueries ? a.group - tile * kQueries : kQueries;
-  const float c = a.scale_log2 * (a.k_scale ? a.k_scale[h] : 1.f);
   for (;;) {
     // What a lane derives from its number is derived anew for each row: kept
     // over the loop it would not fit into the registers.
     uint32_t thread = threadIdx.x;
     asm volatile("" : "+v"(thread));
     const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
-    const int col = lane & 15, grp = lane >> 4;
+    const int col = lane & 15, grp = lane >> 4, jq = thread >> 4;
     Range all = attended(a, b);
     all.begin = __builtin_amdgcn_readfirstlane(all.begin);
     all.end = __builtin_amdgcn_readfirstlane(all.end);
@@ -355,25 +358,28 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
       to = before + tokens > t0 + share ? (int)(t0 + share - before) : tokens;
     }
     if (tokens == 0) {
-      const int jq = thread >> 4;
-      const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
-      if (jq < queries) {
-        uint16_t* dst = (uint16_t*)(a.out + b * a.o_row + (head0 + jq) * a.o_head);
+      for (int hh = h0; hh <= h0 + pair; ++hh) {
+        const int head = hh * a.group + tile * kQueries + jq;
+        if (jq >= queries) break;
+        uint16_t* dst = (uint16_t*)(a.out + b * a.o_row + head * a.o_head);
         for (int d = col; d < a.depth; d += 16) dst[d] = 0;
-        if (col == 0 && a.lse) a.lse[head] = -INFINITY;
+        if (col == 0 && a.lse) a.lse[int64_t(b) * a.heads * a.group + head] = -INFINITY;
       }
     } else {
-      // a wave takes a run of tokens, whole blocks but for the last
-      const int run = (to - from + kWaves * kBlock - 1) / (kWaves * kBlock) * kBlock;
-      const int left = to - from - wave * run;
+      // a wave takes a run of tokens, whole blocks but for the last, of one head
+      const int h = h0 + (wave & pair), runs = kWaves >> pair, nth = wave >> pair;
+      const float c = a.scale_log2 * (a.k_scale ? a.k_scale[h] : 1.f);
+      const int run = (to - from + runs * kBlock - 1) / (runs * kBlock) * kBlock;
+      const int left = to - from - nth * run;
       const int n = left < 0 ? 0 : left < run ? left : run;
-      const uint32_t begin = (uint32_t)(all.begin + from) + wave * run;
+      const uint32_t begin = (uint32_t)(all.begin + from) + nth * run;
       const int blocks = (n + kBlock - 1) / kBlock;
 
       // queries: operand column `col`
       u32x4 qf[DS];
       {
-        const char* q = a.q + b * a.q_row + (head0 + (col < queries ? col : 0)) * a.q_head;
+        const char* q =
+            a.q + b * a.q_row + (h * a.group + tile * kQueries + (col < queries ? col : 0)) * a.q_head;
 #pragma unroll
         for (int s = 0; s < DS; ++s) {
           const u32x4 x = ld16(q + 2 * G::from(s, grp, a.depth));
@@ -586,14 +592,12 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
         compute(blocks - 1, std::false_type{});
       }
 
-      // the four waves' parts, joined: thread (query, col) takes a chunk of the sums
+      // the waves' parts of a head, joined: thread (query, col) takes a chunk of
+      // the sums
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (grp == 0) stats[wave][col] = make_float2(m, sum);
       const bool whole = to - from == tokens;
-      const int jq = thread >> 4;
-      const int64_t head = int64_t(b) * a.heads * a.group + head0 + jq;  // (row, query head)
-      float f[kWaves], top = -INFINITY, total = 0.f;
 #pragma unroll
       for (int piece = 0; piece < G::kEights + G::kFours; ++piece) {
         const int n = piece < G::kEights ? 8 : 4;
@@ -605,65 +609,76 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
             for (int r = 0; r < 4; ++r)
               lds.sums[wave][4 * grp + r][col * n + e] = o[8 * piece + e < G::kDims ? 8 * piece + e : 0][r];
         __syncthreads();
-        if (piece == 0) {
+        for (int hh = h0; hh <= h0 + pair && jq < queries; ++hh) {
+          constexpr int kParts = kWaves >> pair;  // waves (w << pair) + hh - h0
+          float2 st[kParts];
+          float top = -INFINITY, total = 0.f, y[8];
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[w][jq].x);
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
-            f[w] = stats[w][jq].y == 0.f ? 0.f : __builtin_amdgcn_exp2f(stats[w][jq].x - top);
-            total += f[w] * stats[w][jq].y;
+          for (int w = 0; w < kParts; ++w) {
+            st[w] = stats[(w << pair) + hh - h0][jq];
+            top = fmaxf(top, st[w].x);
           }
-        }
-        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = 0.f;
-          if (e < n)
+          for (int e = 0; e < 8; ++e) y[e] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) y[e] += f[w] * lds.sums[w][jq][col * n + e];
-        }
-        if (jq >= queries) continue;
-        int d = 128 * piece + n * col;
-        d = d < a.depth - n ? d : a.depth - n;
-        if (whole) {
-          const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[h] : 1.f) / total;
-          uint16_t z[8];
+          for (int w = 0; w < kParts; ++w) {
+            const float f = st[w].y == 0.f ? 0.f : __builtin_amdgcn_exp2f(st[w].x - top);
+            total += f * st[w].y;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = (uint16_t)T::put(total == 0.f ? 0.f : y[e] * g);
-          char* dst = a.out + b * a.o_row + (head0 + jq) * a.o_head + 2 * d;
-          if (n == 8) __builtin_memcpy(dst, z, 16);
-          else __builtin_memcpy(dst, z, 8);
-          if (piece == 0 && col == 0 && a.lse)
-            a.lse[head] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
-        } else {
-          const int64_t p = (int64_t(head0 + jq) * a.chunks + id) * 2 + (from == 0 ? 1 : 0);
-          float* dst = a.part + p * a.depth + d;
-          if (n == 8) __builtin_memcpy(dst, y, 32);
-          else __builtin_memcpy(dst, y, 16);
-          if (piece == 0 && col == 0) a.stat[p] = make_float2(top, total);
+            for (int e = 0; e < 8; ++e)
+              if (e < n) y[e] += f * lds.sums[(w << pair) + hh - h0][jq][col * n + e];
+          }
+          const int head = hh * a.group + tile * kQueries + jq;
+          int d = 128 * piece + n * col;
+          d = d < a.depth - n ? d : a.depth - n;
+          if (whole) {
+            const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[hh] : 1.f) / total;
+            uint16_t z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = (uint16_t)T::put(total == 0.f ? 0.f : y[e] * g);
+            char* dst = a.out + b * a.o_row + head * a.o_head + 2 * d;
+            if (n == 8) __builtin_memcpy(dst, z, 16);
+            else __builtin_memcpy(dst, z, 8);
+            if (piece == 0 && col == 0 && a.lse)
+              a.lse[int64_t(b) * a.heads * a.group + head] =
+                  total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.69314718056f;
+          } else {
+            const int64_t p = (int64_t(head) * a.chunks + id) * 2 + (from == 0 ? 1 : 0);
+            float* dst = a.part + p * a.depth + d;
+            if (n == 8) __builtin_memcpy(dst, y, 32);
+            else __builtin_memcpy(dst, y, 16);
+            if (piece == 0 && col == 0) a.stat[p] = make_float2(top, total);
+          }
         }
       }
     }
     if (!a.chunks) break;
-    if (before >= t0 && to < tokens) goes_on = make_int2(b, (int)((before + tokens - 1) / share) - (int)id + 1);
+    if (before >= t0) {
+      const int parts = to < tokens ? (int)((before + tokens - 1) / share) - (int)id + 1 : 0;
+      if (a.by_row) {
+        if (h0 == 0 && tile == 0 && threadIdx.x == 0) a.plan[b] = make_int2(id, parts);
+      } else if (parts) {
+        goes_on = make_int2(b, parts);
+      }
+    }
     before += tokens;
     if (++b == a.rows || (before >= t0 + share && !last)) break;
     __syncthreads();  // the sums are read
   }
-  if (a.chunks && h == 0 && tile == 0 && threadIdx.x == 0) a.plan[id] = goes_on;
+  if (a.chunks && !a.by_row && h0 == 0 && tile == 0 && threadIdx.x == 0) a.plan[id] = goes_on;
 }
 
-// One workgroup per chunk and query head: the parts of the row that begins in
-// the chunk and goes on past it, weighted by their maxima.  Wave w takes parts
-// w, w + 4, ..; a lane up to 4 dimensions.
-template <class T>
-__global__ __launch_bounds__(kThreads) void join_kernel(Args a) {
-  __shared__ float sums[kWaves][256];
-  __shared__ float totals[kWaves];
+// One workgroup per row, or chunk, and query head: the parts of a row that was
+// cut, weighted by their maxima.  Wave w takes parts w, w + WAVES, ..; a lane up
+// to 4 dimensions.
+template <class T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void join_kernel(Args a) {
+  __shared__ float sums[WAVES][256];
+  __shared__ float totals[WAVES];
   const int hq = a.heads * a.group;
-  const int chunk = blockIdx.x / hq, h = blockIdx.x - chunk * hq;
-  const int2 plan = a.plan[chunk];
-  const int b = plan.x, parts = plan.y;
+  const int entry = blockIdx.x / hq, h = blockIdx.x - entry * hq;
+  const int2 plan = a.plan[entry];
+  const int b = a.by_row ? entry : plan.x, chunk = a.by_row ? plan.x : entry, parts = plan.y;
   if (parts == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t at = (int64_t(h) * a.chunks + chunk) * 2;
@@ -674,7 +689,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args a) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
 #pragma unroll 4
-  for (int i = wave; i < parts; i += kWaves) {
+  for (int i = wave; i < parts; i += WAVES) {
     const int p = i ? 2 * i : 1;
     const float2 z = stat[p];
     const float f = z.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(z.x - top);
@@ -691,11 +706,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args a) {
   __syncthreads();
   total = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) total += totals[w];
+  for (int w = 0; w < WAVES; ++w) total += totals[w];
   if ((int)threadIdx.x < a.depth) {
     float all_waves = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) all_waves += sums[w][threadIdx.x];
+    for (int w = 0; w < WAVES; ++w) all_waves += sums[w][threadIdx.x];
     const float g = total == 0.f ? 0.f : (a.v_scale ? a.v_scale[h / a.group] : 1.f) / total;
     char* dst = a.out + b * a.o_row + h * a.o_head;
     ((uint16_t*)dst)[threadIdx.x] = (uint16_t)T::put(total == 0.f ? 0.f : all_waves * g);
@@ -725,18 +740,37 @@ int64_t resident(int64_t depth, bool e4m3) {
 // Rows up to this length stay whole: 64 rows of up to 1024 tokens take 33 us so
 // and 37 us cut into chunks; of up to 2000, 61 and 58 (one row of 1200: 19 and 13).
 constexpr int64_t kWholeRows = 1024;
-int64_t chunks_for(int64_t heads, int64_t longest, int64_t room) {
-  if (longest <= kWholeRows || !heads) return 0;
+constexpr int64_t kFewJoins = 1024;
+struct Cut {
+  int64_t chunks;
+  bool pair;
+};
+// Rows of 128 and 256 bytes are read faster by workgroups that take two
+// neighbouring heads (256 or 512 bytes of a token together), though a row then
+// has twice the parts: 64 rows of 1 .. 8192 tokens, bf16, depth 128, 177 us
+// against 185 without (e4m3 rows of up to 131072: 211 against 227); 64 rows of up
+// to 2000, 59.5 against 58.8.  Depth 256 and rows of broken lines lose.
+bool pays_as_pair(int64_t rows, int64_t heads, int64_t tiles, int64_t longest, int64_t depth, bool e4m3, int64_t room) {
+  if (heads % 2 || !(depth == 128 || (depth == 64 && !e4m3))) return false;
+  return (double)rows * longest * heads * tiles >= 2560. * room;  // tokens, as far as the host knows
+}
+Cut cut_for(int64_t rows, int64_t heads, int64_t tiles, int64_t longest, int64_t depth, bool e4m3) {
+  if (longest <= kWholeRows || !heads || !tiles) return Cut{0, false};
   // as many workgroups as are resident at once, so that all end together; with
   // many heads, several times that, so that the last round is a small part
-  const int64_t n = (heads * 8 <= room ? room : 4 * room) / heads;
-  return n < 1 ? 1 : n;
+  const int64_t room = resident(depth, e4m3);
+  const bool pair = pays_as_pair(rows, heads, tiles, longest, depth, e4m3, room);
+  const int64_t groups = heads * tiles >> (pair ? 1 : 0), n = (groups * 8 <= room ? room : 4 * room) / groups;
+  return Cut{n < 1 ? 1 : n, pair};
 }
 
-int64_t plan_bytes(int64_t chunks) { return (chunks * 8 + 255) / 256 * 256; }
+// Entries of the plan that the join walks over: of rows or of chunks, whichever
+// are fewer.
+int64_t plan_entries(int64_t chunks, int64_t rows) { return rows <= chunks ? rows : chunks; }
+int64_t plan_bytes(int64_t chunks, int64_t rows) { return (plan_entries(chunks, rows) * 8 + 255) / 256 * 256; }
 
 int plan(const char* what, const stg_tensor* q, const stg_tensor* k_cache, const stg_tensor* page_table, int64_t window,
-         int64_t max_len, int64_t* tiles, int64_t* chunks, int64_t* bytes) {
+         int64_t max_len, int64_t* tiles, Cut* cut, int64_t* bytes) {
   if (int rc = check_query(what, q, "q")) return rc;
   if (int rc = check_paged_cache(what, k_cache, k_cache, page_table)) return rc;
   const int64_t heads = k_cache->shape[2], depth = q->shape[2];
@@ -754,24 +788,25 @@ int plan(const char* what, const stg_tensor* q, const stg_tensor* k_cache, const
   int64_t longest = page_table->shape[1] * k_cache->shape[1];  // each below 2^31
   if (max_len && max_len < longest) longest = max_len;
   if (window && window < longest) longest = window;
-  *chunks = chunks_for(heads * *tiles, longest, resident(depth, k_cache->dtype == STG_U8));
+  *cut = cut_for(q->shape[0], heads, *tiles, longest, depth, k_cache->dtype == STG_U8);
   int64_t groups;
-  if (__builtin_mul_overflow(*chunks ? *chunks : q->shape[0], heads * *tiles, &groups) ||
-      groups > (int64_t(1) << 31) - 1 || *chunks * q->shape[1] > (int64_t(1) << 31) - 1)
+  if (__builtin_mul_overflow(cut->chunks ? cut->chunks : q->shape[0], heads * *tiles, &groups) ||
+      groups > (int64_t(1) << 31) - 1 || cut->chunks * q->shape[1] > (int64_t(1) << 31) - 1)
     return fail(STG_ERR_RANGE, "%s: too many rows and heads", what);
-  *bytes = *chunks ? plan_bytes(*chunks) + *chunks * q->shape[1] * 2 * (8 + depth * 4) : 0;
+  *bytes = cut->chunks ? plan_bytes(cut->chunks, q->shape[0]) + cut->chunks * q->shape[1] * 2 * (8 + depth * 4) : 0;
   return STG_OK;
 }
 
 template <class T, bool E4M3>
-void launch_attention(const Args& a, uint32_t grid, hipStream_t st) {
+void launch_attention(const Args& a, bool pair, uint32_t grid, hipStream_t st) {
   const auto go = [&](auto kernel) {
     launch_kernel("paged_attention", kernel, dim3(grid), dim3(kThreads), 0, st, a);
   };
   const auto pick = [&](auto ds) {
     constexpr int DS = decltype(ds)::value;
-    if (a.depth == 32 * DS) go(paged_attention_kernel<T, DS, E4M3, false>);
-    else go(paged_attention_kernel<T, DS, E4M3, true>);
+    if (a.depth != 32 * DS) go(paged_attention_kernel<T, DS, E4M3, true, false>);
+    else if (pair) go(paged_attention_kernel<T, DS, E4M3, false, (DS == 4 || (DS == 2 && !E4M3))>);
+    else go(paged_attention_kernel<T, DS, E4M3, false, false>);
   };
   const int steps = (a.depth + 31) / 32;
   if (steps <= 2) pick(std::integral_constant<int, 2>{});
@@ -789,8 +824,9 @@ using namespace stg;
 extern "C" int64_t paged_attention_workspace(const stg_tensor* q, const stg_tensor* k_cache,
                                              const stg_tensor* page_table, int64_t window, int64_t max_len) {
   clear_error();
-  int64_t tiles, chunks, bytes;
-  if (int rc = plan("paged_attention_workspace", q, k_cache, page_table, window, max_len, &tiles, &chunks, &bytes))
+  int64_t tiles, bytes;
+  Cut cut;
+  if (int rc = plan("paged_attention_workspace", q, k_cache, page_table, window, max_len, &tiles, &cut, &bytes))
     return -rc;
   return bytes;
 }
@@ -802,8 +838,9 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
                                void* stream) {
   clear_error();
   const char* what = "paged_attention";
-  int64_t tiles, chunks, bytes;
-  if (int rc = plan(what, q, k_cache, page_table, window, max_len, &tiles, &chunks, &bytes)) return rc;
+  int64_t tiles, bytes;
+  Cut cut;
+  if (int rc = plan(what, q, k_cache, page_table, window, max_len, &tiles, &cut, &bytes)) return rc;
   if (int rc = check_paged_cache(what, k_cache, v_cache, page_table)) return rc;
   if (int rc = check_query(what, out, "out")) return rc;
   if (out->dtype != q->dtype) return fail(STG_ERR_INVALID, "%s: out has another dtype than q", what);
@@ -853,25 +890,31 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
   a.group = (int32_t)(q->shape[1] / k_cache->shape[2]);
   a.tiles = (int32_t)tiles;
   a.depth = (int32_t)q->shape[2];
-  a.chunks = (int32_t)chunks;
+  a.chunks = (int32_t)cut.chunks;
+  a.by_row = q->shape[0] <= cut.chunks;
   a.window = window;
   a.plan = (int2*)workspace;
-  a.stat = (float2*)((char*)workspace + plan_bytes(chunks));
-  a.part = (float*)(a.stat + chunks * q->shape[1] * 2);
-  const int64_t grid = (chunks ? chunks : q->shape[0]) * a.heads * a.tiles;
+  a.stat = (float2*)((char*)workspace + plan_bytes(cut.chunks, q->shape[0]));
+  a.part = (float*)(a.stat + cut.chunks * q->shape[1] * 2);
+  const int64_t grid = (cut.chunks ? cut.chunks : q->shape[0]) * (a.heads >> cut.pair) * a.tiles;
   const hipStream_t st = as_stream(stream);
   const bool e4m3 = k_cache->dtype == STG_U8;
   if (q->dtype == STG_BF16) {
-    if (e4m3) launch_attention<BF16, true>(a, (uint32_t)grid, st);
-    else launch_attention<BF16, false>(a, (uint32_t)grid, st);
+    if (e4m3) launch_attention<BF16, true>(a, cut.pair, (uint32_t)grid, st);
+    else launch_attention<BF16, false>(a, cut.pair, (uint32_t)grid, st);
   } else {
-    if (e4m3) launch_attention<F16, true>(a, (uint32_t)grid, st);
-    else launch_attention<F16, false>(a, (uint32_t)grid, st);
+    if (e4m3) launch_attention<F16, true>(a, cut.pair, (uint32_t)grid, st);
+    else launch_attention<F16, false>(a, cut.pair, (uint32_t)grid, st);
   }
   if (int rc = check_launch(what)) return rc;
-  if (!chunks) return STG_OK;
-  const dim3 joins((uint32_t)(chunks * q->shape[1]));
-  if (q->dtype == STG_BF16) launch_kernel("paged_attention/join", join_kernel<BF16>, joins, dim3(kThreads), 0, st, a);
-  else launch_kernel("paged_attention/join", join_kernel<F16>, joins, dim3(kThreads), 0, st, a);
+  if (!cut.chunks) return STG_OK;
+  // few rows with many parts each: 16 waves on one
+  const int64_t joins = plan_entries(cut.chunks, q->shape[0]) * q->shape[1];
+  const auto join = [&](auto kernel, int waves) {
+    launch_kernel("paged_attention/join", kernel, dim3((uint32_t)joins), dim3(64 * waves), 0, st, a);
+  };
+  const bool few = joins <= kFewJoins;
+  if (q->dtype == STG_BF16) few ? join(join_kernel<BF16, 16>, 16) : join(join_kernel<BF16, 4>, 4);
+  else few ? join(join_kernel<F16, 16>, 16) : join(join_kernel<F16, 4>, 4);
   return check_launch("paged_attention/join");
 }
