@@ -692,29 +692,33 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
   }
 }
 
-// dw[d] = sum of the workgroups' partial sums; 64 columns a workgroup, 16 rows
-// at a time.  blockIdx.y: queries, keys.
+// dw[d] = sum of the workgroups' partial sums; 16 columns a workgroup, 64 rows at
+// a time (few columns, so that there are many workgroups).  blockIdx.y: queries,
+// keys.
+constexpr int kSumCols = 16, kSumRows = 1024 / kSumCols;
 template <class T>
 __global__ __launch_bounds__(1024) void weight_kernel(const float* pq, int nq, void* dwq, const float* pk, int nk,
                                                       void* dwk, int depth, int f32) {
-  __shared__ float sums[16][64];
+  __shared__ float sums[kSumRows][kSumCols + 1];
   const float* p = blockIdx.y ? pk : pq;
   const int n = blockIdx.y ? nk : nq;
   void* dw = blockIdx.y ? dwk : dwq;
   if (!dw) return;
-  const int col = threadIdx.x & 63, row = threadIdx.x >> 6, d = blockIdx.x * 64 + col;
+  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols, d = blockIdx.x * kSumCols + col;
   float s = 0.f;
   if (d < depth)
 #pragma unroll 8
-    for (int i = row; i < n; i += 16) s += p[int64_t(i) * depth + d];
+    for (int i = row; i < n; i += kSumRows) s += p[int64_t(i) * depth + d];
   sums[row][col] = s;
   __syncthreads();
-  if (row == 0 && d < depth) {
-    float all = 0.f;
+  // a wave sums a column
+  const int lane = threadIdx.x & 63, c = threadIdx.x >> 6, at = blockIdx.x * kSumCols + c;
+  float all = sums[lane][c];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) all += sums[i][col];
-    if (f32) ((float*)dw)[d] = all;
-    else store_one<T>((char*)dw + int64_t(d) * T::kBytes, all);
+  for (int k = 1; k < 64; k <<= 1) all += __shfl_xor(all, k);
+  if (lane == 0 && at < depth) {
+    if (f32) ((float*)dw)[at] = all;
+    else store_one<T>((char*)dw + int64_t(at) * T::kBytes, all);
   }
 }
 
@@ -853,13 +857,11 @@ int32_t backward_tokens(const Shape& sh, int rotary) {
 
 // Workgroups of the backward: as many as the chip holds at once (by its
 // registers, 3 waves a SIMD with the norm, 5 without), shared out between
-// queries and keys by their heads; fewer where waves would not have a head for
-// each of their groups of lanes.
+// queries and keys by their heads; fewer where waves would not have a token each.
 constexpr int64_t kSumGroups = 1536, kTurnGroups = 1280;
 int32_t groups_for(const Shape& sh, int64_t heads, int64_t most) {
   if (!heads) return 1;
-  const int64_t per_wave = (64 / sh.lanes + heads - 1) / heads;  // tokens
-  const int64_t n = (sh.tokens + kWaves * per_wave - 1) / (kWaves * per_wave);
+  const int64_t n = (sh.tokens + kWaves - 1) / kWaves;
   return (int32_t)(n < 1 ? 1 : n > most ? most : n);
 }
 void split_groups(const Shape& sh, bool norm, int32_t* nq, int32_t* nk) {
@@ -1035,7 +1037,7 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
   if (int rc = check_launch(what)) return rc;
   if (!sums) return STG_OK;
   with_type(q->dtype, [&](auto type) {
-    launch_kernel("qk_norm_rope_backward/weights", weight_kernel<decltype(type)>, dim3((sh.depth + 63) / 64, 2),
+    launch_kernel("qk_norm_rope_backward/weights", weight_kernel<decltype(type)>, dim3((sh.depth + kSumCols - 1) / kSumCols, 2),
                   dim3(1024), 0, st, (const float*)pq, (int)nq, dq_weight, (const float*)pk, (int)nk, dk_weight,
                   (int)sh.depth, (int)t.weight_f32);
   });

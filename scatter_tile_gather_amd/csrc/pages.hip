@@ -11,7 +11,8 @@
 // What bounds them: moving a page reads and writes planes * page bytes once
 // (HBM); the tables are a few kilobytes, and their kernels are latency.  So
 // each operation is two launches: a plan (the scan) and an apply, in which the
-// workgroups that copy pages also write the tables.
+// workgroups that copy pages also write the tables.  128 forks of 16 planes of
+// 32 KB, with the freeing before them: 34 us, of which 24 are the copy's.
 #include "stg_internal.h"
 
 namespace stg {
@@ -59,13 +60,14 @@ constexpr int kMoveVecs = 4;  // 16-byte vectors a thread holds in flight
 constexpr int64_t kMoveBytes = int64_t(kMoveThreads) * kMoveVecs * 16;
 
 // Workspace, in int32: a header of 64, `counts` (one per scan workgroup),
-// `first` and `second` (one per page), `rank` (one per row).
+// `first` and `second` (one per page), `rank` and `last` (one per row).
 struct PlanSpace {
   int32_t* header;
   int32_t* counts;
   int32_t* first;   // reserve, fork: the free pages; compact: pages that move
   int32_t* second;  // compact: where they move
   int32_t* rank;    // reserve, fork: a row's first index into the free pages, or -1
+  int32_t* last;    // fork: the page that a child copies
 };
 constexpr int kFree = 0, kNeed = 1, kMoves = 2;  // header slots
 
@@ -73,16 +75,17 @@ int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
 int64_t scan_groups(int64_t pages) { return pages ? (pages + kScanPages - 1) / kScanPages : 1; }
 
 int64_t plan_ints(int64_t pages, int64_t n) {
-  return 64 + round64(scan_groups(pages)) + 2 * round64(pages) + round64(n);
+  return 64 + round64(scan_groups(pages)) + 2 * round64(pages) + 2 * round64(n);
 }
 
-PlanSpace plan_space(void* ws, int64_t pages) {
+PlanSpace plan_space(void* ws, int64_t pages, int64_t n) {
   PlanSpace s;
   s.header = (int32_t*)ws;
   s.counts = s.header + 64;
   s.first = s.counts + round64(scan_groups(pages));
   s.second = s.first + round64(pages);
   s.rank = s.second + round64(pages);
+  s.last = s.rank + round64(n);
   return s;
 }
 
@@ -127,11 +130,22 @@ __device__ __forceinline__ int32_t group_scan(int32_t v, int32_t* sums, int32_t*
 // Live pages among pages 4 * (first thread index) .. + 3, as bits.
 __device__ __forceinline__ uint32_t live_bits(const int32_t* refs, int64_t at, int32_t pages) {
   uint32_t bits = 0;
+  if (at + 4 <= pages) {
+    const u32x4 v = ld16((const char*)(refs + at));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (at + i < pages && refs[at + i] > 0) bits |= 1u << i;
+    for (int i = 0; i < 4; ++i) bits |= (int32_t)v[i] > 0 ? 1u << i : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (at + i < pages && refs[at + i] > 0) bits |= 1u << i;
+  }
   return bits;
 }
+
+// Up to this many scan workgroups (65,536 pages) each counts the pages before
+// its own itself, 16 bytes a thread and 4096 pages; a launch that counts them
+// once would take longer.
+constexpr int kSelfCount = 16;
 
 __global__ __launch_bounds__(kScanThreads) void count_live_kernel(const int32_t* refs, int32_t pages, int32_t* counts) {
   __shared__ int32_t sums[kScanThreads / 64];
@@ -139,6 +153,16 @@ __global__ __launch_bounds__(kScanThreads) void count_live_kernel(const int32_t*
   int32_t total;
   group_scan(__popc(live_bits(refs, at, pages)), sums, &total);
   if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+// Live pages below `limit`, a multiple of kScanPages or all pages, by the whole
+// workgroup.
+__device__ __forceinline__ int32_t count_live(const int32_t* refs, int64_t limit, int32_t pages, int32_t* sums) {
+  int32_t v = 0;
+  for (int64_t at = threadIdx.x * 4; at < limit; at += kScanPages) v += __popc(live_bits(refs, at, pages));
+  int32_t total;
+  group_scan(v, sums, &total);
+  return total;
 }
 
 // Sum of counts[0 .. n) by the whole workgroup.
@@ -153,7 +177,8 @@ __device__ __forceinline__ int32_t sum_counts(const int32_t* counts, int32_t n, 
 // The free pages in ascending order -> first[], their number -> header.
 __device__ __forceinline__ void list_free(const int32_t* refs, int32_t pages, int32_t groups, const PlanSpace& s,
                                           int32_t* sums) {
-  const int32_t live_before = groups > 1 ? sum_counts(s.counts, blockIdx.x, sums) : 0;
+  const int32_t live_before = groups > kSelfCount ? sum_counts(s.counts, blockIdx.x, sums)
+                              : blockIdx.x ? count_live(refs, int64_t(blockIdx.x) * kScanPages, pages, sums) : 0;
   const int64_t at = int64_t(blockIdx.x) * kScanPages + threadIdx.x * 4;
   const int32_t here = at >= pages ? 0 : (pages - at < 4 ? (int32_t)(pages - at) : 4);
   const uint32_t free_bits = ~live_bits(refs, at, pages) & ((1u << here) - 1);
@@ -205,39 +230,45 @@ __global__ __launch_bounds__(kScanThreads) void fork_plan_kernel(Table t, const 
   int32_t need = 0;
   for (int64_t i0 = 0; i0 < n; i0 += kScanThreads) {
     const int64_t i = i0 + threadIdx.x;
-    const bool copies = i < n && fork_of(t, lens, slots, pages, parents[i], children[i]).last >= 0;
+    const int32_t last = i < n ? fork_of(t, lens, slots, pages, parents[i], children[i]).last : -1;
     int32_t total;
-    const int32_t rank = need + group_scan(copies ? 1 : 0, sums, &total);
-    if (i < n) s.rank[i] = copies ? rank : -1;
+    const int32_t rank = need + group_scan(last >= 0 ? 1 : 0, sums, &total);
+    if (i < n) {
+      s.rank[i] = last >= 0 ? rank : -1;
+      s.last[i] = last;
+    }
     need += total;
   }
   if (threadIdx.x == 0) s.header[kNeed] = need;
 }
 
 // Copies `bytes` (at most kMoveBytes) with the whole workgroup: all loads
-// first, then the stores.
+// first, then the stores.  Stores are non-temporal; loads too (COLD) where the
+// pages may have lain untouched, but not where they were written a step ago.
+template <bool COLD>
 __device__ __forceinline__ void move_bytes(char* dst, const char* src, int64_t bytes) {
   u32x4 v[kMoveVecs];
 #pragma unroll
   for (int k = 0; k < kMoveVecs; ++k) {
     const int64_t o = (int64_t(k) * kMoveThreads + threadIdx.x) * 16;
-    if (o + 16 <= bytes) v[k] = ld16(src + o);
+    if (o + 16 <= bytes) v[k] = COLD ? ld16_nt(src + o) : ld16(src + o);
   }
 #pragma unroll
   for (int k = 0; k < kMoveVecs; ++k) {
     const int64_t o = (int64_t(k) * kMoveThreads + threadIdx.x) * 16;
-    if (o + 16 <= bytes) st16(dst + o, v[k]);
+    if (o + 16 <= bytes) st16_nt(dst + o, v[k]);
   }
   const int64_t tail = bytes & 15;
   if (threadIdx.x < tail) dst[bytes - tail + threadIdx.x] = src[bytes - tail + threadIdx.x];
 }
 
 // Part `part` (kMoveBytes) of page src in plane `plane` to page dst.
+template <bool COLD>
 __device__ __forceinline__ void move_part(const Planes& c, int32_t src, int32_t dst, int32_t plane, int64_t part) {
   const int64_t o = part * kMoveBytes;
   const int64_t left = c.page_bytes - o;
   char* base = c.data + plane * c.plane_stride + o;
-  move_bytes(base + dst * c.page_stride, base + src * c.page_stride, left < kMoveBytes ? left : kMoveBytes);
+  move_bytes<COLD>(base + dst * c.page_stride, base + src * c.page_stride, left < kMoveBytes ? left : kMoveBytes);
 }
 
 // One workgroup per (fork, plane, part of a page); the first one of a fork
@@ -255,13 +286,13 @@ __global__ __launch_bounds__(kMoveThreads) void fork_apply_kernel(Planes cache, 
   const int64_t steps = per_fork ? per_fork : 1;
   for (int64_t w = blockIdx.x; w < n * steps; w += gridDim.x) {
     const int64_t i = w / steps, r = w - i * steps;
+    const int32_t rank = s.rank[i], last = s.last[i];
+    const int32_t fresh = rank >= 0 && rank < free_pages ? s.first[rank] : -1;
+    if (fresh >= 0 && per_fork) move_part<false>(cache, last, fresh, (int32_t)(r / parts), r % parts);
+    if (r) continue;
     const int32_t p = parents[i], c = children[i];
     const Fork f = fork_of(t, lens, slots, cache.pages, p, c);
     if (!f.ok) continue;
-    const int32_t rank = s.rank[i];
-    const int32_t fresh = rank >= 0 && rank < free_pages ? s.first[rank] : -1;
-    if (fresh >= 0 && per_fork) move_part(cache, f.last, fresh, (int32_t)(r / parts), r % parts);
-    if (r) continue;
     const bool rest = f.len % slots != 0;
     for (int32_t j = threadIdx.x; j < t.width; j += kMoveThreads) {
       int32_t e = -1;
@@ -386,7 +417,7 @@ __global__ __launch_bounds__(kMoveThreads) void copy_kernel(Planes cache, const 
     const int64_t i = w / steps, r = w - i * steps;
     const int32_t a = src[i], b = dst[i];
     if (!in_range(a, cache.pages) || !in_range(b, cache.pages)) continue;
-    move_part(cache, a, b, (int32_t)(r / parts), r % parts);
+    move_part<true>(cache, a, b, (int32_t)(r / parts), r % parts);
   }
 }
 
@@ -404,8 +435,13 @@ __global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(const int32_
   const uint32_t bits = live_bits(refs, at, pages);
   int32_t below = group_scan(__popc(bits), sums, &total);
   if (groups > 1) {
-    live_before = sum_counts(s.counts, blockIdx.x, sums);
-    live = sum_counts(s.counts, groups, sums);
+    const bool counted = groups > kSelfCount;
+    const auto before = [&](int32_t g) {
+      return counted ? sum_counts(s.counts, g, sums)
+                     : count_live(refs, g < groups ? int64_t(g) * kScanPages : pages, pages, sums);
+    };
+    live_before = before(blockIdx.x);
+    live = before(groups);
     const int32_t g = live / kScanPages < groups ? live / kScanPages : groups - 1;  // the group that L lies in
     const int64_t from = int64_t(g) * kScanPages + threadIdx.x * 4;
     const int64_t keep = live - from;  // pages of these four below L
@@ -413,7 +449,7 @@ __global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(const int32_
     b &= keep <= 0 ? 0u : keep >= 4 ? 0xFu : (1u << keep) - 1;
     int32_t inside;
     group_scan(__popc(b), sums, &inside);
-    at_border = inside + sum_counts(s.counts, g, sums);
+    at_border = inside + before(g);
   } else {
     live = total;
     // the thread whose pages hold L, or the last one where L is past them all
@@ -469,13 +505,16 @@ __global__ __launch_bounds__(kMoveThreads) void compact_apply_kernel(Planes cach
   const int64_t steps = cache.planes * parts;
   for (int64_t w = blockIdx.x; w < moves * steps; w += gridDim.x) {
     const int64_t i = w / steps, r = w - i * steps;
-    move_part(cache, s.first[i], s.second[i], (int32_t)(r / parts), r % parts);
+    move_part<true>(cache, s.first[i], s.second[i], (int32_t)(r / parts), r % parts);
   }
 }
 
 // ---- host -------------------------------------------------------------------
 
-constexpr int64_t kMoveGrid = 4096;  // workgroups of a copy: 16 per CU, each loops
+// Workgroups of a copy, which loop.  997 pages in 16 planes of 32 KB: 198 us with
+// 4096 of them, 186 with 32768 (5.6 TB/s read and written, where a copy of one
+// large array reaches 5.8 to 6.1).
+constexpr int64_t kMoveGrid = 32768;
 
 int check_cache(const char* what, const stg_tensor* c) {
   if (int rc = check_tensor(c, "cache")) return rc;
@@ -527,7 +566,7 @@ int64_t product(int64_t a, int64_t b, int64_t c) {
 
 int count_if_many(const char* name, const int32_t* refs, int32_t pages, int32_t groups, const PlanSpace& s,
                   hipStream_t st) {
-  if (groups < 2) return STG_OK;
+  if (groups <= kSelfCount) return STG_OK;
   launch_kernel(name, count_live_kernel, dim3(groups), dim3(kScanThreads), 0, st, refs, pages, s.counts);
   return check_launch(name);
 }
@@ -570,7 +609,7 @@ extern "C" int pages_reserve(const stg_tensor* page_table, const int32_t* seq_le
   const Table t = table_of(page_table);
   if ((t.rows && (!seq_lens || !n_new)) || (n_pages && !refs))
     return fail(STG_ERR_INVALID, "%s: null seq_lens, n_new or refs", what);
-  const PlanSpace s = plan_space(workspace, n_pages);
+  const PlanSpace s = plan_space(workspace, n_pages, t.rows);
   const int32_t groups = (int32_t)scan_groups(n_pages);
   const hipStream_t st = as_stream(stream);
   if (int rc = count_if_many("pages_reserve/count", refs, (int32_t)n_pages, groups, s, st)) return rc;
@@ -597,7 +636,7 @@ extern "C" int pages_fork(const stg_tensor* cache, const stg_tensor* page_table,
     return fail(STG_ERR_INVALID, "%s: null seq_lens, refs, parents or children", what);
   const int64_t parts = parts_of(c), per = product(c.planes, parts, 1), items = product(n, per ? per : 1, 1);
   if (items == INT64_MAX) return fail(STG_ERR_RANGE, "%s: too many pages", what);
-  const PlanSpace s = plan_space(workspace, c.pages);
+  const PlanSpace s = plan_space(workspace, c.pages, n);
   const int32_t groups = (int32_t)scan_groups(c.pages);
   const hipStream_t st = as_stream(stream);
   if (int rc = count_if_many("pages_fork/count", refs, c.pages, groups, s, st)) return rc;
@@ -638,7 +677,7 @@ extern "C" int pages_compact(const stg_tensor* cache, const stg_tensor* page_tab
   const int64_t parts = parts_of(c), items = product(c.pages / 2, c.planes, parts);
   if (items == INT64_MAX) return fail(STG_ERR_RANGE, "%s: too many pages", what);
   if (!c.pages) return STG_OK;
-  const PlanSpace s = plan_space(workspace, c.pages);
+  const PlanSpace s = plan_space(workspace, c.pages, 0);
   const int32_t groups = (int32_t)scan_groups(c.pages);
   const hipStream_t st = as_stream(stream);
   if (int rc = count_if_many("pages_compact/count", refs, c.pages, groups, s, st)) return rc;
