@@ -33,9 +33,15 @@ enum CacheKind { kNoCache = 0, kSameCache = 1, kE4m3Cache = 2 };
 struct Rows {  // (tokens, heads, depth), strides in elements
   char* data;
   int64_t token, head;
+  // Head h of token first + i.  NARROW: strides in bytes are below 2^24 and what
+  // they add to the first token's address below 2^31, so that all but that
+  // address, the same for the wave, is 32-bit arithmetic.
   template <class T>
-  __device__ __forceinline__ char* at(int64_t t, int64_t h) const {
-    return data + (t * token + h * head) * T::kBytes;
+  __device__ __forceinline__ char* at(int64_t first, int i, int h, bool narrow) const {
+    if (narrow)
+      return data + first * token * T::kBytes +
+             (uint32_t)(__mul24(i, (int)token * T::kBytes) + __mul24(h, (int)head * T::kBytes));
+    return data + ((first + i) * token + h * head) * T::kBytes;
   }
 };
 // By value, field by field: a choice between references would put the three
@@ -60,6 +66,7 @@ struct Shape {
   int32_t q_heads, k_heads, depth;
   int32_t lanes;        // L
   int32_t wave_tokens;  // tokens whose heads a wave takes at a time
+  int32_t narrow;       // see Rows::at
 };
 
 struct Cache {
@@ -83,8 +90,13 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 struct BF16 {
   static constexpr int kBytes = 2;
+  static __device__ __forceinline__ uint32_t put2(float x, float y) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), v2));
+  }
   static __device__ __forceinline__ float get(uint32_t bits) { return __uint_as_float(bits << 16); }
   static __device__ __forceinline__ uint32_t put(float x) {
     return __builtin_bit_cast(uint16_t, (__bf16)x);
@@ -92,6 +104,10 @@ struct BF16 {
 };
 struct F16 {
   static constexpr int kBytes = 2;
+  static __device__ __forceinline__ uint32_t put2(float x, float y) {
+    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), v2));
+  }
   static __device__ __forceinline__ float get(uint32_t bits) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
   }
@@ -119,7 +135,11 @@ struct Raw {
 };
 
 // How chunks meet a row's end.
-enum Edge { kWhole = 0, kPart = 1 };  // depth is a multiple of 8; it is not
+enum Edge {
+  kFull = 0,   // depth is 16 L: every lane has two chunks
+  kWhole = 1,  // depth is a multiple of 8
+  kPart = 2    // it is not
+};
 
 // Elements [at, at + 8) of a row of `depth` as far as the row goes (n of them;
 // n <= 0: none, and what is read is not used).  A chunk that would pass the
@@ -127,8 +147,8 @@ enum Edge { kWhole = 0, kPart = 1 };  // depth is a multiple of 8; it is not
 // nothing waits for it; unpack() moves it into place.
 template <class T, int EDGE>
 __device__ __forceinline__ void load_raw(const char* row, int at, int n, int depth, Raw<T>& x) {
-  if (EDGE == kWhole || depth >= 8) {
-    const int from = n >= 8 ? at : n <= 0 ? 0 : depth - 8;
+  if (EDGE != kPart || depth >= 8) {
+    const int from = EDGE == kFull || n >= 8 ? at : n <= 0 ? 0 : depth - 8;
     const char* p = row + from * T::kBytes;
 #pragma unroll
     for (int i = 0; i < T::kBytes / 2; ++i) {
@@ -173,7 +193,7 @@ template <class T, int EDGE>
 __device__ __forceinline__ void unpack(Raw<T> x, int n, int depth, float (&y)[8]) {
   if (EDGE == kPart && depth >= 8) move_down<T>(x, n > 0 && n < 8 ? 8 - n : 0);
 #pragma unroll
-  for (int i = 0; i < 2 * T::kBytes; ++i) x.w[i] = n > 0 ? x.w[i] : 0;
+  for (int i = 0; i < 2 * T::kBytes; ++i) x.w[i] = EDGE == kFull || n > 0 ? x.w[i] : 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (T::kBytes == 4) y[i] = __uint_as_float(x.w[i]);
@@ -213,9 +233,9 @@ __device__ __forceinline__ void store_chunk(char* p, int n, const float (&x)[8])
 #pragma unroll
   for (int i = 0; i < 2 * T::kBytes; ++i) {
     if constexpr (T::kBytes == 4) w[i] = __float_as_uint(x[i]);
-    else w[i] = T::put(x[2 * i]) | T::put(x[2 * i + 1]) << 16;
+    else w[i] = T::put2(x[2 * i], x[2 * i + 1]);
   }
-  if (n >= 8) {
+  if (EDGE == kFull || n >= 8) {
 #pragma unroll
     for (int i = 0; i < T::kBytes / 2; ++i) st16_nt(p + 16 * i, u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
   } else if (EDGE == kPart) {
@@ -257,19 +277,12 @@ __device__ __forceinline__ void store_e4m3(char* p, int n, const float (&x)[8], 
     w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
     w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w[i], true);
   }
-  if (n >= 8) {
+  if (EDGE == kFull || n >= 8) {
     __builtin_memcpy(p, w, 8);
   } else if (EDGE == kPart) {
     const uint32_t u[2] = {(uint32_t)w[0], (uint32_t)w[1]};
     store_part<1>(p, n, u);
   }
-}
-
-// Values are computed here and now, so that the registers that they came from
-// are free for loads that follow.
-__device__ __forceinline__ void settle(float (&a)[8], float (&b)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(a[i]), "+v"(b[i]));
 }
 
 // Sum over the L lanes of a head: within 16 lanes by DPP.
@@ -314,10 +327,14 @@ __device__ __forceinline__ Chunks chunks_of(int sub, int depth, int rotary) {
 // inv_freq is exact in fp64 up to 2^29 positions and is reduced to a quarter
 // turn there, so fp32 sees an angle of at most pi / 4 whatever the position;
 // from there the Taylor series to r^9 and r^10 leave less than 2^-28.
-__device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float2* cs) {
+// For `tokens` tokens, one after the other; a wave's lanes share out all pairs.
+__device__ __forceinline__ void angles_of(const Turn& t, const int32_t* positions, int tokens, float2* cs) {
   const double kPerQuarter = 0.63661977236758134308, kQuarterHi = 1.57079632679489655800, kQuarterLo = 6.12323399573676604e-17;
-  for (int i = threadIdx.x & 63; i < t.rotary >> 1; i += 64) {
-    const double a = (double)position * (double)t.inv_freq[i];
+  const int half = t.rotary >> 1;
+  const float per_half = 1.f / (float)(half ? half : 1);
+  for (int at = threadIdx.x & 63; at < tokens * half; at += 64) {
+    const int tok = (int)(((float)at + 0.5f) * per_half);  // at / half: at < 2^17, so the half outweighs the rounding
+    const double a = (double)positions[tok] * (double)t.inv_freq[at - tok * half];
     const double n = rint(a * kPerQuarter);
     const float r = (float)fma(-n, kQuarterLo, fma(-n, kQuarterHi, a));
     const int quarter = (int)fma(-4.0, floor(n * 0.25), n);
@@ -325,8 +342,15 @@ __device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float
     const float s = fmaf(r * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), r);
     const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
     const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
-    cs[i] = make_float2((quarter + 1) & 2 ? -x * t.gain : x * t.gain, quarter & 2 ? -y * t.gain : y * t.gain);
+    cs[at] = make_float2((quarter + 1) & 2 ? -x * t.gain : x * t.gain, quarter & 2 ? -y * t.gain : y * t.gain);
   }
+}
+
+// Values are computed here and now, so that the registers that they came from
+// are free for loads that follow.
+__device__ __forceinline__ void settle(float (&a)[8], float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(a[i]), "+v"(b[i]));
 }
 
 // Turns a lane's chunks in place; sign -1 turns back.  `swap` is this wave's
@@ -334,31 +358,40 @@ __device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float
 template <int MODE>
 __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Chunks& c, const float2* cs, int rotary,
                                      float sign, float* swap) {
+  // (selects, not branches: merging those would cost more moves than the turn)
   if constexpr (MODE == kHalfInLane) {
-    if (c.a < rotary >> 1) {
+    const bool on = c.a < rotary >> 1;
+    float zc[8], zs[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 z = cs[c.a + i];
-        const float s = sign * z.y, x = a[i], y = b[i];
-        a[i] = x * z.x - y * s;
-        b[i] = y * z.x + x * s;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float2 z = cs[(on ? c.a : 0) + i];
+      zc[i] = z.x, zs[i] = z.y;
+    }
+    settle(zc, zs);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sign * zs[i], x = a[i], y = b[i], u = x * zc[i] - y * s, v = y * zc[i] + x * s;
+      a[i] = on ? u : x;
+      b[i] = on ? v : y;
     }
   } else if constexpr (MODE == kInterleaved) {
+    // a chunk that ends past the turning ones reads up to three pairs more
+    float zc[8], zs[8];  // four of each chunk
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      if (c.a + i < rotary) {
-        const float2 z = cs[(c.a + i) >> 1];
-        const float s = sign * z.y, x = a[i], y = a[i + 1];
-        a[i] = x * z.x - y * s;
-        a[i + 1] = y * z.x + x * s;
-      }
-      if (c.b + i < rotary) {
-        const float2 z = cs[(c.b + i) >> 1];
-        const float s = sign * z.y, x = b[i], y = b[i + 1];
-        b[i] = x * z.x - y * s;
-        b[i + 1] = y * z.x + x * s;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 z = cs[(c.a < rotary ? c.a >> 1 : 0) + i], w = cs[(c.b < rotary ? c.b >> 1 : 0) + i];
+      zc[i] = z.x, zs[i] = z.y;
+      zc[4 + i] = w.x, zs[4 + i] = w.y;
+    }
+    settle(zc, zs);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float(&v)[8] = k < 4 ? a : b;
+      const int i = 2 * (k & 3);
+      const bool on = (k < 4 ? c.a : c.b) + i < rotary;
+      const float s = sign * zs[k], x = v[i], y = v[i + 1], u = x * zc[k] - y * s, w = y * zc[k] + x * s;
+      v[i] = on ? u : x;
+      v[i + 1] = on ? w : y;
     }
   } else {
     const int h = rotary >> 1;
@@ -399,9 +432,9 @@ __device__ __forceinline__ void stage_weight(const void* w, int f32, int depth, 
 // LDS, in floats.  Weights: as many elements as the chunks of L lanes can name.
 __host__ __device__ inline int weight_floats(int lanes) { return lanes * 16 + 8; }
 // One wave's: cos and sin of its tokens, where they go in a cache (keys and
-// values, 64 bits each), the exchange.
+// values, 64 bits each), the exchange (or what a chunk may read past the end).
 __host__ __device__ inline int wave_floats(int rotary, int wave_tokens, int mode, int cache) {
-  return wave_tokens * (rotary + (cache != kNoCache ? 4 : 0)) + (mode == kHalfExchange ? 1024 : 0);
+  return wave_tokens * (rotary + (cache != kNoCache ? 4 : 0)) + (mode == kHalfExchange ? 1024 : 8);
 }
 
 // The items (token, head) that a group of lanes takes, `step` apart.
@@ -456,7 +489,7 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
   const auto fetch = [&](Raw<T>& a, Raw<T>& b) __attribute__((always_inline)) {
     const bool live = ahead.i < tokens;
     const int i = live ? ahead.i : 0, role = live ? role_of(ahead.h) : role_of(0);
-    const char* row = pick(role, q, k, v).at<T>(first + i, live ? head_of(ahead.h, role) : 0);
+    const char* row = pick(role, q, k, v).at<T>(first, i, live ? head_of(ahead.h, role) : 0, sh.narrow);
     load_raw<T, EDGE>(row, c.a, c.na, sh.depth, a);
     load_raw<T, EDGE>(row, c.b, c.nb, sh.depth, b);
     ahead.next(step, heads);
@@ -483,7 +516,7 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
       place[2 * i + 1] = ok ? page * cache.v_page + slot * cache.v_slot : -1;
     }
   }
-  for (int i = 0; i < tokens; ++i) angles_of(t, t.rotary ? positions[first + i] : 0, cs + i * half);
+  angles_of(t, positions + first, tokens, cs);
   __syncthreads();
 
   const float inv_depth = 1.f / (float)sh.depth;
@@ -513,9 +546,8 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
       turn<MODE>(a, b, c, cs + i * half, t.rotary, 1.f, swap);
     }
     if (!live) return;
-    const int64_t tok = first + i;
     if (CACHE == kNoCache || role == 0) {
-      char* dst = pick(role, q_out, k_out, k_out).at<T>(tok, h);
+      char* dst = pick(role, q_out, k_out, k_out).at<T>(first, i, h, sh.narrow);
       store_chunk<T, EDGE>(dst + int64_t(c.a) * T::kBytes, c.na, a);
       store_chunk<T, EDGE>(dst + int64_t(c.b) * T::kBytes, c.nb, b);
       return;
@@ -590,12 +622,12 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
     Raw<T> ya[A], yb[A], va[A], vb[A];
     const auto fetch = [&](int slot) __attribute__((always_inline)) {
       const bool live = ahead.i < tokens;
-      const int64_t tok = first + (live ? ahead.i : 0), h = live ? ahead.h : 0;
-      const char* dy = g.dy.template at<T>(tok, h);
+      const int i = live ? ahead.i : 0, h = live ? ahead.h : 0;
+      const char* dy = g.dy.template at<T>(first, i, h, sh.narrow);
       load_raw<T, EDGE>(dy, c.a, c.na, sh.depth, ya[slot]);
       load_raw<T, EDGE>(dy, c.b, c.nb, sh.depth, yb[slot]);
       if (NORM) {
-        const char* x = g.x.template at<T>(tok, h);
+        const char* x = g.x.template at<T>(first, i, h, sh.narrow);
         load_raw<T, EDGE>(x, c.a, c.na, sh.depth, va[slot]);
         load_raw<T, EDGE>(x, c.b, c.nb, sh.depth, vb[slot]);
       }
@@ -609,8 +641,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
         block = lead.i;
         covered = block + sh.wave_tokens < tokens ? block + sh.wave_tokens : tokens;
         wave_sync();
-        if (half)
-          for (int i = block; i < covered; ++i) angles_of(t, positions[first + i], cs + (i - block) * half);
+        angles_of(t, positions + first + block, covered - block, cs);
         wave_sync();
       }
       const bool live = now.i < tokens;
@@ -655,7 +686,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
         }
       }
       if (live) {
-        char* dx = g.dx.template at<T>(first + i, h);
+        char* dx = g.dx.template at<T>(first, i, h, sh.narrow);
         store_chunk<T, EDGE>(dx + int64_t(c.a) * T::kBytes, c.na, ua);
         store_chunk<T, EDGE>(dx + int64_t(c.b) * T::kBytes, c.nb, ub);
       }
@@ -792,8 +823,9 @@ void with_mode(int mode, F&& f) {
   else f(std::integral_constant<int, kHalfExchange>{});
 }
 template <class F>
-void with_edge(int32_t depth, F&& f) {
-  if (depth % 8 == 0) f(std::integral_constant<int, kWhole>{});
+void with_edge(const Shape& sh, F&& f) {
+  if (sh.depth == 16 * sh.lanes) f(std::integral_constant<int, kFull>{});
+  else if (sh.depth % 8 == 0) f(std::integral_constant<int, kWhole>{});
   else f(std::integral_constant<int, kPart>{});
 }
 template <class F>
@@ -810,6 +842,12 @@ int32_t wave_tokens_for(const Shape& sh, int heads, int rotary) {
   int n = heads > 0 ? (4 * groups + heads - 1) / heads : 1;
   if (rotary && n > 1024 / rotary) n = 1024 / rotary;
   return n < 1 ? 1 : n > 64 ? 64 : n;
+}
+
+// Whether rows can be addressed with 24-bit strides over `tokens` tokens.
+bool narrow(const Rows& x, int64_t tokens, int64_t heads, int32_t dtype) {
+  const int64_t es = dtype_size(dtype), lim = int64_t(1) << 23, token = x.token * es, head = x.head * es;
+  return token < lim && head < lim && tokens < lim && token * tokens + head * heads < (int64_t(1) << 31);
 }
 
 template <int CACHE>
@@ -829,13 +867,17 @@ int launch_forward(const char* what, int32_t dtype, int mode, const Rows& q, con
   int shares = 1;
   while (shares < rounds && blocks * kWaves * shares < 1024) shares *= 2;
   const dim3 grid((uint32_t)blocks, (uint32_t)(shares < rounds ? shares : rounds));
+  sh.narrow = narrow(q, sh.wave_tokens, sh.q_heads, dtype) && narrow(k, sh.wave_tokens, sh.k_heads, dtype) &&
+              (CACHE == kNoCache || narrow(v, sh.wave_tokens, sh.k_heads, dtype)) &&
+              narrow(q_out, sh.wave_tokens, sh.q_heads, dtype) &&
+              (CACHE != kNoCache || narrow(k_out, sh.wave_tokens, sh.k_heads, dtype));
   const uint32_t shmem =
       (2 * weight_floats(sh.lanes) + kWaves * wave_floats(t.rotary, sh.wave_tokens, mode, CACHE)) * 4;
   with_type(dtype, [&](auto type) {
     with_mode(mode, [&](auto m) {
       using T = decltype(type);
       if constexpr (CACHE == kNoCache || T::kBytes == 2)
-        with_edge(sh.depth, [&](auto e) {
+        with_edge(sh, [&](auto e) {
           launch_kernel(what, forward_kernel<T, decltype(m)::value, CACHE, decltype(e)::value>, grid, dim3(kThreads),
                         shmem, st, q, k, v, positions, t, sh, q_out, k_out, cache);
         });
@@ -1015,6 +1057,11 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
   sh.wave_tokens = backward_tokens(sh, t.rotary);
   int32_t nq, nk;
   split_groups(sh, t.norm, &nq, &nk);
+  sh.narrow = 1;
+  for (const stg_tensor* x : {dq_out, q, dq})
+    if (!narrow(rows_of(x), sh.tokens / (int64_t(nq) * kWaves) + 1, sh.q_heads, q->dtype)) sh.narrow = 0;
+  for (const stg_tensor* x : {dk_out, k, dk})
+    if (!narrow(rows_of(x), sh.tokens / (int64_t(nk) * kWaves) + 1, sh.k_heads, q->dtype)) sh.narrow = 0;
   float* pq = (float*)workspace;
   float* pk = pq + int64_t(nq) * sh.depth;
   const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, dq_weight ? pq : nullptr};
@@ -1025,7 +1072,7 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
   if (!sh.tokens && !sums) return STG_OK;
   with_type(q->dtype, [&](auto type) {
     with_mode(mode, [&](auto m) {
-      with_edge(sh.depth, [&](auto e) {
+      with_edge(sh, [&](auto e) {
         const auto go = [&](auto kernel) {
           launch_kernel(what, kernel, dim3(nq + nk), dim3(kThreads), shmem, st, gq, gk, positions, t, sh);
         };
