@@ -327,14 +327,20 @@ __device__ __forceinline__ Chunks chunks_of(int sub, int depth, int rotary) {
 // inv_freq is exact in fp64 up to 2^29 positions and is reduced to a quarter
 // turn there, so fp32 sees an angle of at most pi / 4 whatever the position;
 // from there the Taylor series to r^9 and r^10 leave less than 2^-28.
-// For `tokens` tokens, one after the other; a wave's lanes share out all pairs.
-__device__ __forceinline__ void angles_of(const Turn& t, const int32_t* positions, int tokens, float2* cs) {
+// For up to 64 tokens, one after the other; a wave's lanes share out all pairs.
+// Lane l comes with position l and, where there are no more than 64, frequency
+// l, so that nothing is loaded here.
+__device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float freq, int tokens, float2* cs) {
   const double kPerQuarter = 0.63661977236758134308, kQuarterHi = 1.57079632679489655800, kQuarterLo = 6.12323399573676604e-17;
-  const int half = t.rotary >> 1;
+  const int half = t.rotary >> 1, total = tokens * half;
   const float per_half = 1.f / (float)(half ? half : 1);
-  for (int at = threadIdx.x & 63; at < tokens * half; at += 64) {
+  for (int from = 0; from < total; from += 64) {  // every lane takes part, for the exchange
+    const int at = from + (threadIdx.x & 63);
     const int tok = (int)(((float)at + 0.5f) * per_half);  // at / half: at < 2^17, so the half outweighs the rounding
-    const double a = (double)positions[tok] * (double)t.inv_freq[at - tok * half];
+    const int i = at - tok * half;
+    float f = __shfl(freq, i);
+    if (half > 64) f = t.inv_freq[i];
+    const double a = (double)__shfl(position, tok) * (double)f;
     const double n = rint(a * kPerQuarter);
     const float r = (float)fma(-n, kQuarterLo, fma(-n, kQuarterHi, a));
     const int quarter = (int)fma(-4.0, floor(n * 0.25), n);
@@ -342,7 +348,7 @@ __device__ __forceinline__ void angles_of(const Turn& t, const int32_t* position
     const float s = fmaf(r * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), r);
     const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
     const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
-    cs[at] = make_float2((quarter + 1) & 2 ? -x * t.gain : x * t.gain, quarter & 2 ? -y * t.gain : y * t.gain);
+    if (at < total) cs[at] = make_float2((quarter + 1) & 2 ? -x * t.gain : x * t.gain, quarter & 2 ? -y * t.gain : y * t.gain);
   }
 }
 
@@ -419,14 +425,18 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Chunks&
   }
 }
 
-// A weight (1 where there is none) -> to[0 .. pitch), by the whole workgroup.
+// A weight's element d, 1 where there is none.
 template <class T>
-__device__ __forceinline__ void stage_weight(const void* w, int f32, int depth, int pitch, float* to) {
-  for (int d = threadIdx.x; d < pitch; d += kThreads) {
-    float x = 1.f;
-    if (w && d < depth) x = f32 ? ((const float*)w)[d] : load_one<T>((const char*)w + int64_t(d) * T::kBytes);
-    to[d] = x;
-  }
+__device__ __forceinline__ float weight_at(const void* w, int f32, int depth, int d) {
+  if (!w || d >= depth) return 1.f;
+  return f32 ? ((const float*)w)[d] : load_one<T>((const char*)w + int64_t(d) * T::kBytes);
+}
+// The weight -> to[0 .. pitch), by the whole workgroup; mine: this thread's first
+// element, which it has already.
+template <class T>
+__device__ __forceinline__ void stage_weight(float mine, const void* w, int f32, int depth, int pitch, float* to) {
+  if ((int)threadIdx.x < pitch) to[threadIdx.x] = mine;
+  for (int d = threadIdx.x + kThreads; d < pitch; d += kThreads) to[d] = weight_at<T>(w, f32, depth, d);
 }
 
 // LDS, in floats.  Weights: as many elements as the chunks of L lanes can name.
@@ -494,29 +504,41 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
     load_raw<T, EDGE>(row, c.b, c.nb, sh.depth, b);
     ahead.next(step, heads);
   };
+  // what comes before the first head, on its way together and ahead of the heads
+  int32_t position = 0;
+  int64_t row = first + lane;
+  float freq = 0.f, wq = 1.f, wk = 1.f;
+  if (lane < tokens) {
+    if (positions) position = positions[first + lane];
+    if (CACHE != kNoCache && cache.token_rows) row = cache.token_rows[first + lane];
+  }
+  if (lane < half) freq = t.inv_freq[lane];
+  if (t.norm) {
+    wq = weight_at<T>(t.wq, t.weight_f32, sh.depth, threadIdx.x);
+    wk = weight_at<T>(t.wk, t.weight_f32, sh.depth, threadIdx.x);
+  }
   if (rounds) {
 #pragma unroll
     for (int i = 0; i < A; ++i) fetch(ra[i], rb[i]);
   }
 
-  if (t.norm) {
-    stage_weight<T>(t.wq, t.weight_f32, sh.depth, pitch, lds);
-    stage_weight<T>(t.wk, t.weight_f32, sh.depth, pitch, lds + pitch);
-  }
   if constexpr (CACHE != kNoCache) {
-    for (int i = lane; i < tokens; i += 64) {
-      const int64_t tok = first + i, row = cache.token_rows ? cache.token_rows[tok] : tok;
-      const int32_t pos = positions[tok], entry = pos / cache.slots;
+    if (lane < tokens) {
+      const int32_t entry = position / cache.slots;
       int32_t page = -1;
-      if (row >= 0 && row < cache.rows && pos >= 0 && entry < cache.width)
+      if (row >= 0 && row < cache.rows && position >= 0 && entry < cache.width)
         page = cache.table[row * cache.table_stride + entry];
-      const int64_t slot = pos - entry * cache.slots;
+      const int64_t slot = position - entry * cache.slots;
       const bool ok = (uint32_t)page < (uint32_t)cache.pages;
-      place[2 * i] = ok ? page * cache.k_page + slot * cache.k_slot : -1;
-      place[2 * i + 1] = ok ? page * cache.v_page + slot * cache.v_slot : -1;
+      place[2 * lane] = ok ? page * cache.k_page + slot * cache.k_slot : -1;
+      place[2 * lane + 1] = ok ? page * cache.v_page + slot * cache.v_slot : -1;
     }
   }
-  angles_of(t, positions + first, tokens, cs);
+  if (t.norm) {
+    stage_weight<T>(wq, t.wq, t.weight_f32, sh.depth, pitch, lds);
+    stage_weight<T>(wk, t.wk, t.weight_f32, sh.depth, pitch, lds + pitch);
+  }
+  angles_of(t, position, freq, tokens, cs);
   __syncthreads();
 
   const float inv_depth = 1.f / (float)sh.depth;
@@ -607,13 +629,16 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
   float sa[8], sb[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sa[e] = sb[e] = 0.f;
-  if (NORM) stage_weight<T>(g.w, t.weight_f32, sh.depth, pitch, lds);
-  __syncthreads();
   const float inv_depth = 1.f / (float)sh.depth;
   const int64_t run = (sh.tokens + int64_t(g.groups) * kWaves - 1) / (int64_t(g.groups) * kWaves);
   const int64_t first = (int64_t(group_id) * kWaves + wave) * run, left = sh.tokens - first;
   const int tokens = (int)(left < 0 ? 0 : left < run ? left : run);
   const int total = tokens * g.heads, rounds = (total + groups - 1) / groups;
+  const float freq = lane < half ? t.inv_freq[lane] : 0.f;
+  if (NORM) {
+    stage_weight<T>(weight_at<T>(g.w, t.weight_f32, sh.depth, threadIdx.x), g.w, t.weight_f32, sh.depth, pitch, lds);
+    __syncthreads();
+  }
   if (rounds) {
     Item now(group, g.heads), ahead = now;
     const Item step(groups, g.heads);
@@ -640,8 +665,9 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
       if (need >= covered) {
         block = lead.i;
         covered = block + sh.wave_tokens < tokens ? block + sh.wave_tokens : tokens;
+        const int32_t position = half && lane < covered - block ? positions[first + block + lane] : 0;
         wave_sync();
-        angles_of(t, positions + first + block, covered - block, cs);
+        angles_of(t, position, freq, covered - block, cs);
         wave_sync();
       }
       const bool live = now.i < tokens;
@@ -892,7 +918,7 @@ int32_t backward_tokens(const Shape& sh, int rotary) {
   const int groups = 64 / sh.lanes;
   int heads = sh.q_heads;
   if (!heads || (sh.k_heads && sh.k_heads < heads)) heads = sh.k_heads;
-  const int touched = groups == 1 || !heads ? 1 : (groups - 1) / heads + 2;
+  const int touched = groups == 1 || !heads ? 1 : heads == 1 ? groups : (groups - 1) / heads + 2;  // at most 64
   const int n = rotary ? 1024 / rotary : 8;
   return touched > n ? touched : n < 8 ? n : touched > 8 ? touched : 8;
 }
