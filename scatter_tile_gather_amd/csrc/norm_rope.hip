@@ -136,9 +136,10 @@ struct Raw {
 
 // How chunks meet a row's end.
 enum Edge {
-  kFull = 0,   // depth is 16 L: every lane has two chunks
-  kWhole = 1,  // depth is a multiple of 8
-  kPart = 2    // it is not
+  kLines = 0,  // depth is 16 L, and the lanes' first (or second) chunks are whole cache lines together
+  kFull = 1,   // depth is 16 L: every lane has two chunks
+  kWhole = 2,  // depth is a multiple of 8
+  kPart = 3    // it is not
 };
 
 // Elements [at, at + 8) of a row of `depth` as far as the row goes (n of them;
@@ -148,11 +149,13 @@ enum Edge {
 template <class T, int EDGE>
 __device__ __forceinline__ void load_raw(const char* row, int at, int n, int depth, Raw<T>& x) {
   if (EDGE != kPart || depth >= 8) {
-    const int from = EDGE == kFull || n >= 8 ? at : n <= 0 ? 0 : depth - 8;
+    const int from = EDGE <= kFull || n >= 8 ? at : n <= 0 ? 0 : depth - 8;
     const char* p = row + from * T::kBytes;
 #pragma unroll
     for (int i = 0; i < T::kBytes / 2; ++i) {
-      const u32x4 v = ld16(p + 16 * i);
+      // gradients of 16384 tokens, 40 heads of 128, bf16: 101 us with non-temporal
+      // loads, 105 without; of depth 64, whose loads take half lines, 71 and 66
+      const u32x4 v = EDGE == kLines ? ld16_nt(p + 16 * i) : ld16(p + 16 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) x.w[4 * i + j] = v[j];
     }
@@ -193,7 +196,7 @@ template <class T, int EDGE>
 __device__ __forceinline__ void unpack(Raw<T> x, int n, int depth, float (&y)[8]) {
   if (EDGE == kPart && depth >= 8) move_down<T>(x, n > 0 && n < 8 ? 8 - n : 0);
 #pragma unroll
-  for (int i = 0; i < 2 * T::kBytes; ++i) x.w[i] = EDGE == kFull || n > 0 ? x.w[i] : 0;
+  for (int i = 0; i < 2 * T::kBytes; ++i) x.w[i] = EDGE <= kFull || n > 0 ? x.w[i] : 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (T::kBytes == 4) y[i] = __uint_as_float(x.w[i]);
@@ -235,7 +238,7 @@ __device__ __forceinline__ void store_chunk(char* p, int n, const float (&x)[8])
     if constexpr (T::kBytes == 4) w[i] = __float_as_uint(x[i]);
     else w[i] = T::put2(x[2 * i], x[2 * i + 1]);
   }
-  if (EDGE == kFull || n >= 8) {
+  if (EDGE <= kFull || n >= 8) {
 #pragma unroll
     for (int i = 0; i < T::kBytes / 2; ++i) st16_nt(p + 16 * i, u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]});
   } else if (EDGE == kPart) {
@@ -277,7 +280,7 @@ __device__ __forceinline__ void store_e4m3(char* p, int n, const float (&x)[8], 
     w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
     w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w[i], true);
   }
-  if (EDGE == kFull || n >= 8) {
+  if (EDGE <= kFull || n >= 8) {
     __builtin_memcpy(p, w, 8);
   } else if (EDGE == kPart) {
     const uint32_t u[2] = {(uint32_t)w[0], (uint32_t)w[1]};
@@ -848,8 +851,11 @@ void with_mode(int mode, F&& f) {
   else if (mode == kInterleaved) f(std::integral_constant<int, kInterleaved>{});
   else f(std::integral_constant<int, kHalfExchange>{});
 }
-template <class F>
+template <class T, class F>
 void with_edge(const Shape& sh, F&& f) {
+  if constexpr (T::kBytes == 2) {
+    if (sh.depth == 16 * sh.lanes && sh.lanes >= 8) return f(std::integral_constant<int, kLines>{});
+  }
   if (sh.depth == 16 * sh.lanes) f(std::integral_constant<int, kFull>{});
   else if (sh.depth % 8 == 0) f(std::integral_constant<int, kWhole>{});
   else f(std::integral_constant<int, kPart>{});
@@ -903,7 +909,7 @@ int launch_forward(const char* what, int32_t dtype, int mode, const Rows& q, con
     with_mode(mode, [&](auto m) {
       using T = decltype(type);
       if constexpr (CACHE == kNoCache || T::kBytes == 2)
-        with_edge(sh, [&](auto e) {
+        with_edge<T>(sh, [&](auto e) {
           launch_kernel(what, forward_kernel<T, decltype(m)::value, CACHE, decltype(e)::value>, grid, dim3(kThreads),
                         shmem, st, q, k, v, positions, t, sh, q_out, k_out, cache);
         });
@@ -1098,7 +1104,7 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
   if (!sh.tokens && !sums) return STG_OK;
   with_type(q->dtype, [&](auto type) {
     with_mode(mode, [&](auto m) {
-      with_edge(sh, [&](auto e) {
+      with_edge<decltype(type)>(sh, [&](auto e) {
         const auto go = [&](auto kernel) {
           launch_kernel(what, kernel, dim3(nq + nk), dim3(kThreads), shmem, st, gq, gk, positions, t, sh);
         };
