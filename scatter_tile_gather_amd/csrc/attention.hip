@@ -167,6 +167,10 @@ __device__ __forceinline__ void wave_sync() {
 
 __device__ __forceinline__ void put_words(uint32_t* w, u32x4 x) { w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3]; }
 __device__ __forceinline__ void put_words(uint32_t* w, u32x2 x) { w[0] = x[0], w[1] = x[1]; }
+// Loads above stay above: the compiler would move plain ones into the next
+// iteration, to where they are used.
+__device__ __forceinline__ void stay() { asm volatile("" ::: "memory"); }
+
 // From an address in global memory, at any alignment; NT: non-temporal.
 template <class V, bool NT>
 __device__ __forceinline__ V load_as(int64_t address) {
@@ -577,7 +581,10 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
           product(r1, o[d + 2], o[d + 3]);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) load_values(blk + 1);
+        if (more) {
+          load_values(blk + 1);
+          stay();
+        }
       };
       if (blocks > 0) {
         fetch(0);
@@ -588,6 +595,7 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
         if (blocks > kSpanBlocks) fetch(1);
         load_keys(0);
         load_values(0);
+        stay();
         for (int blk = 0; blk + 1 < blocks; ++blk) compute(blk, std::true_type{});
         compute(blocks - 1, std::false_type{});
       }
