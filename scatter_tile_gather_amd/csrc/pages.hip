@@ -684,7 +684,8 @@ extern "C" int pages_compact(const stg_tensor* cache, const stg_tensor* page_tab
   launch_kernel("pages_compact/plan", compact_plan_kernel, dim3(groups), dim3(kScanThreads), 0, st,
                 (const int32_t*)refs, c.pages, groups, remap, s);
   if (int rc = check_launch("pages_compact/plan")) return rc;
-  launch_kernel("pages_compact", compact_apply_kernel, dim3((uint32_t)kMoveGrid), dim3(kMoveThreads), 0, st, c, t, refs,
-                remap, parts, s);
+  const int64_t entries = (int64_t(t.rows) * t.width + kMoveThreads - 1) / kMoveThreads;
+  launch_kernel("pages_compact", compact_apply_kernel, dim3(grid_of(items > entries ? items : entries)),
+                dim3(kMoveThreads), 0, st, c, t, refs, remap, parts, s);
   return check_launch("pages_compact");
 }
