@@ -91,6 +91,7 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 struct BF16 {
   static constexpr int kBytes = 2;
   static __device__ __forceinline__ uint32_t put2(float x, float y) {
@@ -333,6 +334,8 @@ __device__ __forceinline__ Chunks chunks_of(int sub, int depth, int rotary) {
 // For up to 64 tokens, one after the other; a wave's lanes share out all pairs.
 // Lane l comes with position l and, where there are no more than 64, frequency
 // l, so that nothing is loaded here.
+// MODE kHalfExchange: an entry for every element, sines with their signs.
+template <int MODE>
 __device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float freq, int tokens, float2* cs) {
   const double kPerQuarter = 0.63661977236758134308, kQuarterHi = 1.57079632679489655800, kQuarterLo = 6.12323399573676604e-17;
   const int half = t.rotary >> 1, total = tokens * half;
@@ -351,7 +354,14 @@ __device__ __forceinline__ void angles_of(const Turn& t, int32_t position, float
     const float s = fmaf(r * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), r);
     const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
     const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
-    if (at < total) cs[at] = make_float2((quarter + 1) & 2 ? -x * t.gain : x * t.gain, quarter & 2 ? -y * t.gain : y * t.gain);
+    const float ct = (quarter + 1) & 2 ? -x * t.gain : x * t.gain, st = quarter & 2 ? -y * t.gain : y * t.gain;
+    if (at >= total) break;
+    if constexpr (MODE == kHalfExchange) {
+      cs[at + tok * half] = make_float2(ct, -st);
+      cs[at + tok * half + half] = make_float2(ct, st);
+    } else {
+      cs[at] = make_float2(ct, st);
+    }
   }
 }
 
@@ -403,26 +413,40 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Chunks&
       v[i + 1] = on ? w : y;
     }
   } else {
+    // element d's partner is d + h below h, d - h from there on; cs has an entry
+    // for each element, with the sign of its sine
     const int h = rotary >> 1;
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c.a + i < rotary) swap[c.a + i] = a[i];
-      if (c.b + i < rotary) swap[c.b + i] = b[i];
+    for (int k = 0; k < 2; ++k) {
+      const float(&v)[8] = k ? b : a;
+      f32x4* to = (f32x4*)(swap + (k ? c.b : c.a));
+      to[0] = f32x4{v[0], v[1], v[2], v[3]};
+      to[1] = f32x4{v[4], v[5], v[6], v[7]};
     }
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int da = c.a + i, db = c.b + i;
-      if (da < rotary) {
-        const float2 z = cs[da < h ? da : da - h];
-        const float s = sign * z.y;
-        a[i] = da < h ? a[i] * z.x - swap[da + h] * s : a[i] * z.x + swap[da - h] * s;
+    for (int k = 0; k < 2; ++k) {
+      float(&v)[8] = k ? b : a;
+      const int at = k ? c.b : c.a;
+      // (of the sixteen read, those are used that are partners; the others lie
+      // within the exchange and its margins)
+      const f32x2* up = (const f32x2*)(swap + (at < h ? at + h : 0));
+      const f32x2* down = (const f32x2*)(swap + (at + 8 > h ? at - h : 0));
+      const float2* z = cs + (at < rotary ? at : 0);
+      float other[8], zc[8], zs[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = up[i >> 1][i & 1], d = down[i >> 1][i & 1];
+        other[i] = at + i < h ? u : d;
+        zc[i] = z[i].x, zs[i] = z[i].y;
       }
-      if (db < rotary) {
-        const float2 z = cs[db < h ? db : db - h];
-        const float s = sign * z.y;
-        b[i] = db < h ? b[i] * z.x - swap[db + h] * s : b[i] * z.x + swap[db - h] * s;
+      settle(zc, zs);
+      settle(other, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = v[i] * zc[i] + other[i] * (sign * zs[i]);
+        v[i] = at + i < rotary ? y : v[i];
       }
     }
   }
@@ -442,12 +466,14 @@ __device__ __forceinline__ void stage_weight(float mine, const void* w, int f32,
   for (int d = threadIdx.x + kThreads; d < pitch; d += kThreads) to[d] = weight_at<T>(w, f32, depth, d);
 }
 
+constexpr int kMargin = 16;  // floats before and after the exchange
 // LDS, in floats.  Weights: as many elements as the chunks of L lanes can name.
 __host__ __device__ inline int weight_floats(int lanes) { return lanes * 16 + 8; }
 // One wave's: cos and sin of its tokens, where they go in a cache (keys and
 // values, 64 bits each), the exchange (or what a chunk may read past the end).
 __host__ __device__ inline int wave_floats(int rotary, int wave_tokens, int mode, int cache) {
-  return wave_tokens * (rotary + (cache != kNoCache ? 4 : 0)) + (mode == kHalfExchange ? 1024 : 8);
+  if (mode == kHalfExchange) return wave_tokens * (2 * rotary + (cache != kNoCache ? 4 : 0)) + 1024 + 2 * kMargin;
+  return wave_tokens * (rotary + (cache != kNoCache ? 4 : 0)) + 8;
 }
 
 // The items (token, head) that a group of lanes takes, `step` apart.
@@ -480,11 +506,11 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
   constexpr int A = 2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int L = sh.lanes, sub = lane & (L - 1), group = lane / L, groups = 64 / L;
-  const int pitch = weight_floats(L), half = t.rotary >> 1;
+  const int pitch = weight_floats(L), half = t.rotary >> 1, per = MODE == kHalfExchange ? t.rotary : half;
   float* own = lds + 2 * pitch + wave * wave_floats(t.rotary, sh.wave_tokens, MODE, CACHE);
   int64_t* place = (int64_t*)own;  // of key and value, per token
   float2* cs = (float2*)(own + (CACHE != kNoCache ? 4 * sh.wave_tokens : 0));
-  float* swap = (float*)cs + sh.wave_tokens * t.rotary + group * L * 16;
+  float* swap = (float*)cs + 2 * sh.wave_tokens * t.rotary + kMargin + group * L * 16;
   const int64_t first = (int64_t(blockIdx.x) * kWaves + wave) * sh.wave_tokens;
   const int tokens = first >= sh.tokens ? 0 : sh.tokens - first < sh.wave_tokens ? (int)(sh.tokens - first) : sh.wave_tokens;
   const Chunks c = chunks_of<MODE>(sub, sh.depth, t.rotary);
@@ -541,7 +567,7 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
     stage_weight<T>(wq, t.wq, t.weight_f32, sh.depth, pitch, lds);
     stage_weight<T>(wk, t.wk, t.weight_f32, sh.depth, pitch, lds + pitch);
   }
-  angles_of(t, position, freq, tokens, cs);
+  angles_of<MODE>(t, position, freq, tokens, cs);
   __syncthreads();
 
   const float inv_depth = 1.f / (float)sh.depth;
@@ -568,7 +594,7 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Rows q, Rows k, Rows 
           b[e] *= r * w[c.b + e];
         }
       }
-      turn<MODE>(a, b, c, cs + i * half, t.rotary, 1.f, swap);
+      turn<MODE>(a, b, c, cs + i * per, t.rotary, 1.f, swap);
     }
     if (!live) return;
     if (CACHE == kNoCache || role == 0) {
@@ -608,6 +634,7 @@ struct Gradient {  // queries or keys
   const void* w;
   int32_t heads;
   int32_t groups;   // workgroups on it
+  int64_t run;      // heads of all tokens that a wave takes
   float* partial;   // (groups, depth) or null
 };
 
@@ -625,31 +652,34 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
   const int group_id = keys ? blockIdx.x - dq.groups : blockIdx.x;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int L = sh.lanes, sub = lane & (L - 1), group = lane / L, groups = 64 / L;
-  const int pitch = weight_floats(L), half = t.rotary >> 1;
+  const int pitch = weight_floats(L), half = t.rotary >> 1, per = MODE == kHalfExchange ? t.rotary : half;
   float2* cs = (float2*)(lds + pitch + wave * wave_floats(t.rotary, sh.wave_tokens, MODE, kNoCache));
-  float* swap = (float*)cs + sh.wave_tokens * t.rotary + group * L * 16;
+  float* swap = (float*)cs + 2 * sh.wave_tokens * t.rotary + kMargin + group * L * 16;
   const Chunks c = chunks_of<MODE>(sub, sh.depth, t.rotary);
   float sa[8], sb[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sa[e] = sb[e] = 0.f;
   const float inv_depth = 1.f / (float)sh.depth;
-  const int64_t run = (sh.tokens + int64_t(g.groups) * kWaves - 1) / (int64_t(g.groups) * kWaves);
-  const int64_t first = (int64_t(group_id) * kWaves + wave) * run, left = sh.tokens - first;
-  const int tokens = (int)(left < 0 ? 0 : left < run ? left : run);
-  const int total = tokens * g.heads, rounds = (total + groups - 1) / groups;
+  // a run of heads of all tokens; tokens: those that it touches, from `first` on
+  const int64_t start = (int64_t(group_id) * kWaves + wave) * g.run, left = sh.tokens * g.heads - start;
+  const int total = (int)(left < 0 ? 0 : left < g.run ? left : g.run), rounds = (total + groups - 1) / groups;
+  const int64_t first = total <= 0 ? 0 : start >> 32 ? start / g.heads : (uint32_t)start / (uint32_t)g.heads;
+  const int skip = (int)(start - first * g.heads), tokens = total ? (skip + total - 1) / g.heads + 1 : 0;
   const float freq = lane < half ? t.inv_freq[lane] : 0.f;
   if (NORM) {
     stage_weight<T>(weight_at<T>(g.w, t.weight_f32, sh.depth, threadIdx.x), g.w, t.weight_f32, sh.depth, pitch, lds);
     __syncthreads();
   }
   if (rounds) {
-    Item now(group, g.heads), ahead = now;
+    Item now(skip + group, g.heads), ahead = now;
     const Item step(groups, g.heads);
-    Item lead(0, g.heads), tail(groups - 1, g.heads);  // of a round: its first item and its last
+    Item lead(skip, g.heads), tail(skip + groups - 1, g.heads);  // of a round: its first item and its last
+    int mine = group, fetched = group;                           // this group's place in the run
     int block = 0, covered = 0;                        // tokens whose angles are in LDS: [block, covered)
     Raw<T> ya[A], yb[A], va[A], vb[A];
     const auto fetch = [&](int slot) __attribute__((always_inline)) {
-      const bool live = ahead.i < tokens;
+      const bool live = fetched < total;
+      fetched += groups;
       const int i = live ? ahead.i : 0, h = live ? ahead.h : 0;
       const char* dy = g.dy.template at<T>(first, i, h, sh.narrow);
       load_raw<T, EDGE>(dy, c.a, c.na, sh.depth, ya[slot]);
@@ -670,10 +700,11 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
         covered = block + sh.wave_tokens < tokens ? block + sh.wave_tokens : tokens;
         const int32_t position = half && lane < covered - block ? positions[first + block + lane] : 0;
         wave_sync();
-        angles_of(t, position, freq, covered - block, cs);
+        angles_of<MODE>(t, position, freq, covered - block, cs);
         wave_sync();
       }
-      const bool live = now.i < tokens;
+      const bool live = mine < total;
+      mine += groups;
       const int i = live ? now.i : lead.i, h = now.h;
       now.next(step, g.heads);
       lead.next(step, g.heads);
@@ -689,7 +720,7 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradien
       if (NORM) settle(xa, xb);
       __builtin_amdgcn_sched_barrier(0);
       fetch(slot);
-      turn<MODE>(ua, ub, c, cs + (i - block) * half, t.rotary, -1.f, swap);
+      turn<MODE>(ua, ub, c, cs + (i - block) * per, t.rotary, -1.f, swap);
       if (NORM) {
         // with r = 1 / sqrt(mean(x^2) + eps): dx = r u w - x r^3 mean(u w x)
         float ss = 0.f, sd = 0.f;
@@ -931,11 +962,11 @@ int32_t backward_tokens(const Shape& sh, int rotary) {
 
 // Workgroups of the backward: as many as the chip holds at once (by its
 // registers, 3 waves a SIMD with the norm, 5 without), shared out between
-// queries and keys by their heads; fewer where waves would not have a token each.
+// queries and keys by their heads; fewer where waves would not have a round each.
 constexpr int64_t kSumGroups = 1536, kTurnGroups = 1280;
 int32_t groups_for(const Shape& sh, int64_t heads, int64_t most) {
   if (!heads) return 1;
-  const int64_t n = (sh.tokens + kWaves - 1) / kWaves;
+  const int64_t wave_heads = int64_t(kWaves) * (64 / sh.lanes), n = (sh.tokens * heads + wave_heads - 1) / wave_heads;
   return (int32_t)(n < 1 ? 1 : n > most ? most : n);
 }
 void split_groups(const Shape& sh, bool norm, int32_t* nq, int32_t* nk) {
@@ -944,6 +975,19 @@ void split_groups(const Shape& sh, bool norm, int32_t* nq, int32_t* nk) {
   q = q < 1 ? 1 : q > all - 1 ? all - 1 : q;
   *nq = groups_for(sh, sh.q_heads, q);
   *nk = groups_for(sh, sh.k_heads, all - q);
+}
+
+// Heads of all tokens that a wave takes.  Where there are several tokens' for
+// each, whole tokens: runs that start anywhere measured 110 us for 102 at 16384
+// tokens of 32 + 8 heads of 128.  Else, and where a token is less than a round,
+// whole rounds, which may start inside a token: one token of 192 heads takes
+// 7.5 us, 35 with a wave to the token, and 9000 of 3 + 3 heads of 72 in f32
+// take 33 us, 44 with whole tokens.
+int64_t run_for(const Shape& sh, int64_t heads, int64_t groups) {
+  const int64_t waves = groups * kWaves, even = (sh.tokens * heads + waves - 1) / waves;
+  const int64_t round = 64 / sh.lanes;
+  const int64_t unit = heads >= round && even > 2 * heads ? heads : round;
+  return (even + unit - 1) / unit * unit;
 }
 
 }  // namespace
@@ -1091,13 +1135,13 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
   split_groups(sh, t.norm, &nq, &nk);
   sh.narrow = 1;
   for (const stg_tensor* x : {dq_out, q, dq})
-    if (!narrow(rows_of(x), sh.tokens / (int64_t(nq) * kWaves) + 1, sh.q_heads, q->dtype)) sh.narrow = 0;
+    if (!narrow(rows_of(x), sh.tokens / (int64_t(nq) * kWaves) + 70, sh.q_heads, q->dtype)) sh.narrow = 0;
   for (const stg_tensor* x : {dk_out, k, dk})
-    if (!narrow(rows_of(x), sh.tokens / (int64_t(nk) * kWaves) + 1, sh.k_heads, q->dtype)) sh.narrow = 0;
+    if (!narrow(rows_of(x), sh.tokens / (int64_t(nk) * kWaves) + 70, sh.k_heads, q->dtype)) sh.narrow = 0;
   float* pq = (float*)workspace;
   float* pk = pq + int64_t(nq) * sh.depth;
-  const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, dq_weight ? pq : nullptr};
-  const Gradient gk{rows_of(dk_out), rows_of(k), rows_of(dk), t.wk, sh.k_heads, nk, dk_weight ? pk : nullptr};
+  const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, run_for(sh, sh.q_heads, nq), dq_weight ? pq : nullptr};
+  const Gradient gk{rows_of(dk_out), rows_of(k), rows_of(dk), t.wk, sh.k_heads, nk, run_for(sh, sh.k_heads, nk), dk_weight ? pk : nullptr};
   const hipStream_t st = as_stream(stream);
   uint32_t shmem = (weight_floats(sh.lanes) + kWaves * wave_floats(t.rotary, sh.wave_tokens, mode, kNoCache)) * 4;
   if (shmem < kWaves * (uint32_t)sh.depth * 4) shmem = kWaves * sh.depth * 4;
