@@ -11,9 +11,10 @@
 //    and values, where a kernel that only reads rows of 256 bytes so reaches 6.7
 //    to 7.1); cut row by row into parts of 1024 tokens it took 18 us more.
 //  - Its four waves each take a quarter of a row's tokens (or half of them for
-//    one of two neighbouring heads, see pays_as_pair) and walk over blocks of 32.  A block's keys and values are loaded into registers while the
-//    block before is computed; its addresses come from LDS, a span of 128
-//    tokens ahead.  There is no barrier in the loop.
+//    one of two neighbouring heads, see pays_as_pair) and walk over blocks of
+//    32.  A block's keys and values are loaded into registers while the block
+//    before is computed; its addresses come from LDS, a span of 128 tokens
+//    ahead.  There is no barrier in the loop.
 //  - Scores are computed transposed, S^T = K Q^T (v_mfma 16x16x32): a lane then
 //    holds, for query l % 16, the scores of 8 of the 32 tokens -- just the
 //    elements that the second product wants as its left operand P, so
@@ -22,9 +23,10 @@
 //    them in any order as long as V is fed in the same one.
 //  - Loads cover whole rows, 256 contiguous bytes in 16 lanes: read as matrix
 //    operands straight away, K would come in pieces of 64 bytes of 16 rows, and
-//    that cost a seventh.  K's rows become operands through LDS.  V is wanted with 8 tokens of one dimension in a lane but lies
-//    with 8 dimensions of one token in 16 bytes: a lane loads 8 x 8 elements and
-//    transposes them with byte permutes in its own registers.
+//    that cost a seventh.  K's rows become operands through LDS.  V is wanted
+//    with 8 tokens of one dimension in a lane but lies with 8 dimensions of one
+//    token in 16 bytes: a lane loads 8 x 8 elements and transposes them with
+//    byte permutes in its own registers.
 //  - Where rows are whole cache lines, loads are non-temporal (an eighth faster).
 //    Where they are not, neighbouring heads share lines: then the heads of a
 //    token run on one XCD, whose L2 keeps the line for the next (depth 100,
@@ -168,7 +170,8 @@ __device__ __forceinline__ void wave_sync() {
 __device__ __forceinline__ void put_words(uint32_t* w, u32x4 x) { w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3]; }
 __device__ __forceinline__ void put_words(uint32_t* w, u32x2 x) { w[0] = x[0], w[1] = x[1]; }
 // Loads above stay above: the compiler would move plain ones into the next
-// iteration, to where they are used.
+// iteration, to where they are used (8-bit pages of depth 160, 69 rows of up to
+// 339 tokens, 45 heads on 15: 64 us so, 32 as they stand).
 __device__ __forceinline__ void stay() { asm volatile("" ::: "memory"); }
 
 // From an address in global memory, at any alignment; NT: non-temporal.

@@ -11,9 +11,18 @@
 //  - in the half layout a lane holds chunks i and i + R/16, so both elements
 //    of its pairs are its own; interleaved pairs lie inside a chunk.  Only a
 //    half layout whose R / 2 is not a multiple of 8 exchanges elements, through
-//    LDS.
+//    LDS, as vectors (2782 tokens of 9 heads of 192, 124 turned: 15.5 us, 20
+//    with an element at a time).
 //  - cosine and sine depend on the token and the pair alone: the wave that
 //    owns a token computes them once, into LDS, for all heads.
+//  - a wave has two heads' loads on their way while it computes one, and its
+//    stores do not stay in the caches (both together: 72 us for 121, at the 16384
+//    tokens below).
+// Measured, bf16, 32 + 8 heads of 128: 16384 tokens with keys and values into
+// pages 77 us (403 MB, 5.2 TB/s, where a copy reaches 5.8 to 6.1); their backward
+// 102 us with the weights' sums (503 MB, 4.9 TB/s); 64 tokens into 8-bit pages
+// 5.9 us, of which 2.3 are any launch's.  Far from whole rows' lines the loads
+// bound it sooner: 8191 tokens of 20 heads of 96, 63 MB, 16 us.
 #include <math.h>
 
 #include <cmath>
@@ -638,10 +647,10 @@ struct Gradient {  // queries or keys
   float* partial;   // (groups, depth) or null
 };
 
-// Workgroups 0 .. dq.groups-1 take queries, the others keys.  A wave has a run
-// of tokens and walks over their heads, summing u x' for the weight in
-// registers; loads are ahead as in the forward kernel, for the whole run, and
-// the angles of wave_tokens tokens are computed as the walk reaches them.
+// Workgroups 0 .. dq.groups-1 take queries, the others keys.  A wave walks over
+// a run of heads (see run_for), summing u x' for the weight in registers; loads
+// are ahead as in the forward kernel, for the whole run, and the angles of
+// wave_tokens tokens are computed as the walk reaches them.
 template <class T, int MODE, int EDGE, bool NORM>
 __global__ __launch_bounds__(kThreads) void backward_kernel(Gradient dq, Gradient dk, const int32_t* positions, Turn t,
                                                             Shape sh) {
@@ -960,9 +969,11 @@ int32_t backward_tokens(const Shape& sh, int rotary) {
   return touched > n ? touched : n < 8 ? n : touched > 8 ? touched : 8;
 }
 
-// Workgroups of the backward: as many as the chip holds at once (by its
-// registers, 3 waves a SIMD with the norm, 5 without), shared out between
-// queries and keys by their heads; fewer where waves would not have a round each.
+// Workgroups of the backward, shared out between queries and keys by their
+// heads; fewer where waves would not have a round each.  Without the norm as
+// many as the chip holds at once (5 a compute unit, by its registers), with it
+// twice that (3): at 16384 tokens of 32 + 8 heads of 128, 102 us, 110 with 768
+// and 107 with 2048.
 constexpr int64_t kSumGroups = 1536, kTurnGroups = 1280;
 int32_t groups_for(const Shape& sh, int64_t heads, int64_t most) {
   if (!heads) return 1;
@@ -1140,8 +1151,10 @@ extern "C" int qk_norm_rope_backward(const stg_tensor* dq_out, const stg_tensor*
     if (!narrow(rows_of(x), sh.tokens / (int64_t(nk) * kWaves) + 70, sh.k_heads, q->dtype)) sh.narrow = 0;
   float* pq = (float*)workspace;
   float* pk = pq + int64_t(nq) * sh.depth;
-  const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, run_for(sh, sh.q_heads, nq), dq_weight ? pq : nullptr};
-  const Gradient gk{rows_of(dk_out), rows_of(k), rows_of(dk), t.wk, sh.k_heads, nk, run_for(sh, sh.k_heads, nk), dk_weight ? pk : nullptr};
+  const Gradient gq{rows_of(dq_out), rows_of(q), rows_of(dq), t.wq, sh.q_heads, nq, run_for(sh, sh.q_heads, nq),
+                    dq_weight ? pq : nullptr};
+  const Gradient gk{rows_of(dk_out), rows_of(k), rows_of(dk), t.wk, sh.k_heads, nk, run_for(sh, sh.k_heads, nk),
+                    dk_weight ? pk : nullptr};
   const hipStream_t st = as_stream(stream);
   uint32_t shmem = (weight_floats(sh.lanes) + kWaves * wave_floats(t.rotary, sh.wave_tokens, mode, kNoCache)) * 4;
   if (shmem < kWaves * (uint32_t)sh.depth * 4) shmem = kWaves * sh.depth * 4;
