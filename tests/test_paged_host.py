@@ -70,7 +70,7 @@ def test_attention_of_nothing_and_workspace(lib):
     need = lambda width, window, hint: lib.paged_attention_workspace(B(q), B(k), B(t([4, width], I32)), window, hint)  # noqa: E731
     assert need(1, 0, 0) == 0
     full = need(5000, 0, 0)
-    assert full > 0 and full % ((64 + 2) * 4 * 4 * 8) == 0  # whole parts of depth + 2 floats per row and head
+    assert full >= (64 + 2) * 4 * 4 * 8  # at least depth + 2 floats per row and head
     assert need(5000, 100, 0) == 0 and need(5000, 0, 200) == 0
     assert 0 < need(5000, 0, 2000) <= full
     assert need(5000, -1, 0) == -INVALID
