@@ -680,11 +680,13 @@ __global__ __launch_bounds__(kThreads, waves_for(DS, E4M3)) void paged_attention
 }
 
 // One workgroup per row, or chunk, and query head: the parts of a row that was
-// cut, weighted by their maxima.  Wave w takes parts w, w + WAVES, ..; a lane up
-// to 4 dimensions.
-template <class T, int WAVES>
+// cut, weighted by their maxima.  Wave w takes parts w, w + WAVES, ..; a lane
+// D dimensions.  Latency bounds it, so four parts' loads go out together, none of
+// them conditional (past the end they read the first part again): 256 parts of
+// depth 256 for 10 heads take 7.7 us, 27 one after the other.
+template <class T, int WAVES, int D>
 __global__ __launch_bounds__(64 * WAVES) void join_kernel(Args a) {
-  __shared__ float sums[WAVES][256];
+  __shared__ float sums[WAVES][64 * D];
   __shared__ float totals[WAVES];
   const int hq = a.heads * a.group;
   const int entry = blockIdx.x / hq, h = blockIdx.x - entry * hq;
@@ -695,24 +697,45 @@ __global__ __launch_bounds__(64 * WAVES) void join_kernel(Args a) {
   const int64_t at = (int64_t(h) * a.chunks + chunk) * 2;
   const float2* stat = a.stat + at;
   const float* part = a.part + at * a.depth;
-  float top = -INFINITY, total = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = lane; i < parts; i += 64) top = fmaxf(top, stat[i ? 2 * i : 1].x);
+  float top = -INFINITY, total = 0.f, y[D];
+#pragma unroll
+  for (int e = 0; e < D; ++e) y[e] = 0.f;
+  int dim[D];
+#pragma unroll
+  for (int e = 0; e < D; ++e) dim[e] = lane + 64 * e < a.depth ? lane + 64 * e : 0;
+  for (int i = lane; i < parts + lane; i += 4 * 64) {
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = i + 64 * j;
+      x[j] = stat[k > 0 && k < parts ? 2 * k : 1].x;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, x[j]);
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-#pragma unroll 4
-  for (int i = wave; i < parts; i += WAVES) {
-    const int p = i ? 2 * i : 1;
-    const float2 z = stat[p];
-    const float f = z.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(z.x - top);
-    total += f * z.y;
+  for (int i = wave; i < parts; i += 4 * WAVES) {
+    float2 z[4];
+    float v[4][D];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = lane + 64 * e;
-      if (d < a.depth) y[e] += f * part[int64_t(p) * a.depth + d];
+    for (int j = 0; j < 4; ++j) {
+      const int k = i + WAVES * j, p = k > 0 && k < parts ? 2 * k : 1;
+      z[j] = stat[p];
+#pragma unroll
+      for (int e = 0; e < D; ++e) v[j][e] = part[int64_t(p) * a.depth + dim[e]];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool live = i + WAVES * j < parts;
+      const float f = !live || z[j].y == 0.f ? 0.f : __builtin_amdgcn_exp2f(z[j].x - top);
+      total += f * z[j].y;
+#pragma unroll
+      for (int e = 0; e < D; ++e) y[e] += live ? f * v[j][e] : 0.f;
     }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) sums[wave][lane + 64 * e] = y[e];
+  for (int e = 0; e < D; ++e) sums[wave][lane + 64 * e] = y[e];
   if (lane == 0) totals[wave] = total;
   __syncthreads();
   total = 0.f;
@@ -924,8 +947,16 @@ extern "C" int paged_attention(const stg_tensor* q, const stg_tensor* k_cache, c
   const auto join = [&](auto kernel, int waves) {
     launch_kernel("paged_attention/join", kernel, dim3((uint32_t)joins), dim3(64 * waves), 0, st, a);
   };
-  const bool few = joins <= kFewJoins;
-  if (q->dtype == STG_BF16) few ? join(join_kernel<BF16, 16>, 16) : join(join_kernel<BF16, 4>, 4);
-  else few ? join(join_kernel<F16, 16>, 16) : join(join_kernel<F16, 4>, 4);
+  const auto pick = [&](auto type, auto d) {
+    using T = decltype(type);
+    constexpr int D = decltype(d)::value;
+    joins <= kFewJoins ? join(join_kernel<T, 16, D>, 16) : join(join_kernel<T, 4, D>, 4);
+  };
+  const auto by_depth = [&](auto type) {
+    if (a.depth <= 64) pick(type, std::integral_constant<int, 1>{});
+    else if (a.depth <= 128) pick(type, std::integral_constant<int, 2>{});
+    else pick(type, std::integral_constant<int, 4>{});
+  };
+  q->dtype == STG_BF16 ? by_depth(BF16{}) : by_depth(F16{});
   return check_launch("paged_attention/join");
 }
